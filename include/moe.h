@@ -462,6 +462,57 @@ MOE_API int moe_route_static(const moe_config* cfg, const void* x, const float* 
                              const float* bias, int32_t* topk_idx, float* topk_gate,
                              void* stream);
 
+/* ---- few tokens, 4-bit weights -------------------------------------------- */
+
+/* The whole layer for at most MOE_FEW_MAX_T tokens (a decode step): what
+ * moe_forward computes, from the same packed weights, as one pass over the
+ * weights of the experts the batch hits [only the chosen experts are computed:
+ * Mixtral 8x7B and MoE explained, "Easy explanation" ¶4].  Arguments as in
+ * moe_forward, without slot_of; stats may be NULL (two launches less).  H stays
+ * on the chip and reaches the down projection as two bf16 parts whatever
+ * cfg->hidden_mode says.  Routing outputs equal moe_forward's (gates to fp32
+ * rounding); repeated calls give identical bits.
+ * Errors besides those of every call, before any launch: MOE_ERR_SHAPE for
+ * T > MOE_FEW_MAX_T, MOE_ERR_DTYPE for an fp32 config, MOE_ERR_UNSUPPORTED for
+ * the reroute policy or train = 1.  ws: moe_few_workspace_size(cfg) bytes,
+ * 256-byte aligned; its first word is the device status (moe_read_device_status). */
+#define MOE_FEW_MAX_T 16
+MOE_API int moe_few_workspace_size(const moe_config* cfg, size_t* bytes);
+MOE_API int moe_forward_few(const moe_config* cfg, const void* x, const float* Wr,
+                            const float* bias, const void* W13, const void* W2p,
+                            const void* W13s, const void* W2s, void* out, int32_t* topk_idx,
+                            float* topk_gate, int32_t* routed, int32_t* kept, moe_stats* stats,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* The pages name quantization as a serving lever (wiki entry, "Adoption").
+ * Expert weights in 4 bits with one scale per group of `group` (32, 64 or 128)
+ * weights along the reduction (d for W13 rows, the hidden width for W2p rows):
+ *   s = bf16(max |w| / 7),  q = w / s rounded to nearest even, clamped to
+ *   [-7, 7] (0 where s = 0);  the weight's value is q s.
+ * moe_q4_quantize makes one set from packed bf16 weights: which = 0 the routed
+ * experts (W13 [E][2h][d], W2p [E][d][h]), which = 1 the fused shared expert,
+ * both as moe_pack_weights leaves them; weights must be finite.  Q13 and Q2 take
+ * the bytes moe_q4_size gives; their layout is the library's own.
+ * moe_q4_dequantize writes the values, rounded once to bf16, in the packed
+ * layout: moe_forward on them is the layer for batches of any length.  */
+MOE_API int moe_q4_size(const moe_config* cfg, int which, int32_t group, size_t* bytes13,
+                        size_t* bytes2);
+MOE_API int moe_q4_quantize(const moe_config* cfg, int which, int32_t group, const void* W13,
+                            const void* W2p, void* Q13, void* Q2, void* stream);
+MOE_API int moe_q4_dequantize(const moe_config* cfg, int which, int32_t group, const void* Q13,
+                              const void* Q2, void* W13, void* W2p, void* stream);
+
+/* moe_forward_few on 4-bit weights (Q13s / Q2s: the shared set, NULL without
+ * shared experts).  The products take the values q s exactly (q in bf16, the
+ * group's scale in fp32 on its partial sum); nothing is rounded that
+ * moe_forward_few does not round.  MOE_ERR_ARG for another group. */
+MOE_API int moe_forward_few_q4(const moe_config* cfg, int32_t group, const void* x,
+                               const float* Wr, const float* bias, const void* Q13,
+                               const void* Q2, const void* Q13s, const void* Q2s, void* out,
+                               int32_t* topk_idx, float* topk_gate, int32_t* routed,
+                               int32_t* kept, moe_stats* stats, void* ws, size_t ws_bytes,
+                               void* stream);
+
 /* ---- status, tracing, limits ------------------------------------------- */
 
 /* Copies the device status word from ws to *status (MOE_OK or

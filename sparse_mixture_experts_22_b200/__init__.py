@@ -19,4 +19,6 @@ from .binding import (  # noqa: F401
     moe_pack_weights, moe_perm_rows, moe_read_device_status, moe_route, moe_set_wait_limit_ns,
     moe_stats_finalize, moe_stats_sums, moe_trace_begin, moe_trace_end, moe_workspace_size,
     pack_weights, stats_dict,
+    FewLayer, MOE_FEW_MAX_T, dequantize_weights, moe_few_workspace_size, moe_forward_few,
+    moe_forward_few_q4, moe_q4_dequantize, moe_q4_quantize, moe_q4_size, quantize_weights,
 )

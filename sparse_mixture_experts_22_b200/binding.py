@@ -31,9 +31,12 @@ EXPORTS = ["moe_capacity", "moe_workspace_size", "moe_perm_rows", "moe_ffn_split
            "moe_launch_count", "moe_segment_pad", "moe_route_counts", "moe_dispatch_capped",
            "moe_grouped_workspace_size", "moe_expert_ffn_grouped", "moe_combine_rows", "moe_set_pdl",
            "moe_dispatch_peers", "moe_combine_peers", "moe_hidden_split", "moe_set_pair_tiles",
-           "moe_ep_plan", "moe_set_shared_overlap", "moe_set_shared_sms"]
+           "moe_ep_plan", "moe_set_shared_overlap", "moe_set_shared_sms",
+           "moe_few_workspace_size", "moe_forward_few", "moe_forward_few_q4", "moe_q4_size",
+           "moe_q4_quantize", "moe_q4_dequantize"]
 
 MOE_MAX_PEERS = 64
+MOE_FEW_MAX_T = 16
 
 
 class MoEError(RuntimeError):
@@ -115,6 +118,12 @@ def load() -> ctypes.CDLL:
                                        ctypes.c_int32, P, P, P, P, S, P],
             "moe_backward": [C, P, ctypes.c_float, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P,
                              P, P, P, P, P, P, P, P, S, P],
+            "moe_few_workspace_size": [C, P],
+            "moe_forward_few": [C] + [P] * 14 + [S, P],
+            "moe_forward_few_q4": [C, ctypes.c_int32] + [P] * 14 + [S, P],
+            "moe_q4_size": [C, I, ctypes.c_int32, P, P],
+            "moe_q4_quantize": [C, I, ctypes.c_int32, P, P, P, P, P],
+            "moe_q4_dequantize": [C, I, ctypes.c_int32, P, P, P, P, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -275,6 +284,46 @@ def moe_backward(cfg, grad_out, aux_coef, x, Wr, bias, W13t, W2t, W13st, W2st, t
         _p(slot_of), _p(ws), ws.numel() * ws.element_size(), _p(dx), _p(dWr), _p(db), _p(dW13),
         _p(dW2p), _p(dW13s), _p(dW2s), _p(dlogits), _p(bws), bws.numel() * bws.element_size(),
         _stream(stream)))
+
+
+def moe_few_workspace_size(cfg: MoEConfig) -> int:
+    v = ctypes.c_size_t()
+    _check(load().moe_few_workspace_size(ctypes.byref(cfg), ctypes.byref(v)))
+    return v.value
+
+
+def moe_forward_few(cfg, x, Wr, bias, W13, W2p, W13s, W2s, out, topk_idx, topk_gate, routed,
+                    kept, stats, ws, stream=None):
+    _check(load().moe_forward_few(ctypes.byref(cfg), _p(x), _p(Wr), _p(bias), _p(W13), _p(W2p),
+                                  _p(W13s), _p(W2s), _p(out), _p(topk_idx), _p(topk_gate),
+                                  _p(routed), _p(kept), _p(stats), _p(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_forward_few_q4(cfg, group, x, Wr, bias, Q13, Q2, Q13s, Q2s, out, topk_idx, topk_gate,
+                       routed, kept, stats, ws, stream=None):
+    _check(load().moe_forward_few_q4(ctypes.byref(cfg), int(group), _p(x), _p(Wr), _p(bias),
+                                     _p(Q13), _p(Q2), _p(Q13s), _p(Q2s), _p(out), _p(topk_idx),
+                                     _p(topk_gate), _p(routed), _p(kept), _p(stats), _p(ws),
+                                     ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_q4_size(cfg: MoEConfig, which: int, group: int) -> Tuple[int, int]:
+    """Bytes of (Q13, Q2) of one set (which: 0 routed, 1 shared)."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().moe_q4_size(ctypes.byref(cfg), which, int(group), ctypes.byref(a),
+                              ctypes.byref(b)))
+    return a.value, b.value
+
+
+def moe_q4_quantize(cfg, which, group, W13, W2p, Q13, Q2, stream=None):
+    _check(load().moe_q4_quantize(ctypes.byref(cfg), which, int(group), _p(W13), _p(W2p),
+                                  _p(Q13), _p(Q2), _stream(stream)))
+
+
+def moe_q4_dequantize(cfg, which, group, Q13, Q2, W13, W2p, stream=None):
+    _check(load().moe_q4_dequantize(ctypes.byref(cfg), which, int(group), _p(Q13), _p(Q2),
+                                    _p(W13), _p(W2p), _stream(stream)))
 
 
 def moe_read_device_status(ws, stream=None) -> int:
@@ -499,3 +548,154 @@ def backward(cfg: MoEConfig, grad_out, aux_coef, x, Wr, bias, W13t, W2t, W13st, 
                  grads["dW13"], grads["dW2p"], grads.get("dW13s"), grads.get("dW2s"),
                  grads["dlogits"], grads["bws"], stream)
     return grads
+
+
+# ---------------------------------------------------------------- few tokens, 4-bit weights
+
+def _want(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
+    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device
+            or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _packed_shapes(cfg: MoEConfig, shared: bool):
+    hid = cfg.n_shared * cfg.h_shared
+    if shared:
+        return (2 * hid, cfg.d), (cfg.d, hid)
+    return (cfg.E, 2 * cfg.h, cfg.d), (cfg.E, cfg.d, cfg.h)
+
+
+def quantize_weights(cfg: MoEConfig, W13, W2p, group: int = 128, shared: bool = False, out=None,
+                     stream=None):
+    """4-bit form (Q13, Q2) of packed bf16 weights (routed, or the fused shared
+    set), into `out` if given; runs on the weights' device."""
+    sizes = moe_q4_size(cfg, 1 if shared else 0, group)
+    dev = W13.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    for W, name, shape in zip((W13, W2p), ("W13", "W2p"), _packed_shapes(cfg, shared)):
+        # the shared set may come with a leading 1, as one expert of the routed layout
+        _want(W.squeeze(0) if shared and W.dim() == 3 else W, name, shape, torch.bfloat16, dev)
+    if out is None:
+        out = tuple(torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes)
+    for q, name, n in zip(out, ("Q13", "Q2"), sizes):
+        _want(q, name, (n,), torch.uint8, dev)
+    with torch.cuda.device(dev):
+        moe_q4_quantize(cfg, 1 if shared else 0, group, W13, W2p, *out, stream)
+    return out
+
+
+def dequantize_weights(cfg: MoEConfig, Q13, Q2, group: int = 128, shared: bool = False, out=None,
+                       stream=None):
+    """Packed bf16 weights (W13, W2p) of a 4-bit set, into `out` if given: what
+    moe_forward takes for batches longer than MOE_FEW_MAX_T."""
+    sizes = moe_q4_size(cfg, 1 if shared else 0, group)
+    dev = Q13.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    for q, name, n in zip((Q13, Q2), ("Q13", "Q2"), sizes):
+        _want(q, name, (n,), torch.uint8, dev)
+    shapes = _packed_shapes(cfg, shared)
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
+    for W, name, shape in zip(out, ("W13", "W2p"), shapes):
+        _want(W, name, shape, torch.bfloat16, dev)
+    with torch.cuda.device(dev):
+        moe_q4_dequantize(cfg, 1 if shared else 0, group, Q13, Q2, *out, stream)
+    return out
+
+
+class FewLayer:
+    """The layer for batches of up to cfg.T <= MOE_FEW_MAX_T tokens, bound once to
+    its weights, workspace and outputs (moe_forward_few; with `group`, the
+    weights are 4-bit sets of quantize_weights: moe_forward_few_q4).
+
+    layer(x) with x [t, d] bf16, t <= cfg.T, returns views of the layer's own
+    output buffers (out, topk_idx, topk_gate, routed, kept and, with_stats,
+    stats), overwritten by the next call.  The capacity of a call counts its t
+    tokens.  A call runs on the weights' device and, unless a stream is given,
+    on that device's current stream; the layer's buffers are shared by its
+    calls, so calls on several streams must be ordered by the caller."""
+
+    def __init__(self, cfg: MoEConfig, Wr, bias, W13, W2p, W13s=None, W2s=None,
+                 group: Optional[int] = None, with_stats: bool = False):
+        dev = Wr.device
+        if dev.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        self._lib = load()
+        self.cfg, self.group, self.device = cfg, group, dev
+        moe_few_workspace_size(cfg)  # refuses what the layer does not take
+        weights = [W13, W2p] + ([W13s, W2s] if cfg.n_shared else [])
+        if any(w is None for w in weights):
+            raise ValueError("the config's weights are missing (shared experts included)")
+        for i, (w, name) in enumerate(zip(weights, ("W13", "W2p", "W13s", "W2s"))):
+            shared = i >= 2
+            if group is None:
+                shape, dt = _packed_shapes(cfg, shared)[i % 2], torch.bfloat16
+                w = w.squeeze(0) if shared and w.dim() == 3 else w
+            else:
+                shape, dt = (moe_q4_size(cfg, 1 if shared else 0, group)[i % 2],), torch.uint8
+            _want(w, name, shape, dt, dev)
+        _want(Wr, "Wr", (cfg.d, cfg.E), torch.float32, dev)
+        if cfg.has_bias:
+            _want(bias, "bias", (cfg.E,), torch.float32, dev)
+        self._held = (Wr, bias, *weights)
+        T, E, k, d = cfg.T, cfg.E, cfg.k, cfg.d
+        self.bufs = {
+            "out": torch.empty((T, d), dtype=torch.bfloat16, device=dev),
+            "topk_idx": torch.empty((T, k), dtype=torch.int32, device=dev),
+            "topk_gate": torch.empty((T, k), dtype=torch.float32, device=dev),
+            "routed": torch.empty(E, dtype=torch.int32, device=dev),
+            "kept": torch.empty(E, dtype=torch.int32, device=dev),
+        }
+        if with_stats:
+            self.bufs["stats"] = torch.zeros(len(STATS_FIELDS), dtype=torch.float64, device=dev)
+        # the largest batch does not always need the largest workspace
+        need = max(moe_few_workspace_size(self._config(t)) for t in range(T + 1))
+        self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        self._calls: Dict[int, tuple] = {}
+
+    def _config(self, t: int) -> MoEConfig:
+        c = MoEConfig.from_buffer_copy(self.cfg)
+        c.T = t
+        return c
+
+    def _call(self, t: int):
+        cfg, b = self._config(t), self.bufs
+        Wr, bias, W13, W2p, *shared = self._held
+        W13s, W2s = shared if shared else (None, None)
+        views = {n: (v[:t] if n in ("out", "topk_idx", "topk_gate") else v) for n, v in b.items()}
+        tail = [_p(Wr), _p(bias) if cfg.has_bias else None, _p(W13), _p(W2p), _p(W13s), _p(W2s),
+                _p(b["out"]), _p(b["topk_idx"]), _p(b["topk_gate"]), _p(b["routed"]),
+                _p(b["kept"]), _p(b.get("stats")), _p(self.ws), self.ws.numel()]
+        ref = ctypes.byref(cfg)
+        if self.group is None:
+            fn, head = self._lib.moe_forward_few, (ref,)
+        else:
+            fn, head = self._lib.moe_forward_few_q4, (ref, self.group)
+        self._calls[t] = (fn, head, tail, views, cfg)
+        return self._calls[t]
+
+    def __call__(self, x: torch.Tensor, stream=None) -> Dict[str, torch.Tensor]:
+        if (x.dim() != 2 or x.shape[0] > self.cfg.T or x.shape[1] != self.cfg.d
+                or x.dtype != torch.bfloat16 or x.device != self.device or not x.is_contiguous()):
+            raise ValueError(f"x: expected a contiguous bfloat16 tensor of at most "
+                             f"({self.cfg.T}, {self.cfg.d}) on {self.device}, got {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
+        fn, head, tail, views, _ = self._calls.get(x.shape[0]) or self._call(x.shape[0])
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._run(fn, head, tail, views, x, stream)
+        return self._run(fn, head, tail, views, x, stream)
+
+    def _run(self, fn, head, tail, views, x, stream):
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device).cuda_stream
+        elif isinstance(stream, torch.cuda.Stream):
+            stream = stream.cuda_stream
+        rc = fn(*head, x.data_ptr(), *tail, stream)
+        if rc:
+            _check(rc)
+        return views

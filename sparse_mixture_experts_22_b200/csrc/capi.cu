@@ -16,6 +16,7 @@
 
 #include "../../include/moe.h"
 #include "common.cuh"
+#include "few.h"
 #include "kernels.h"
 #include "plan.h"
 
@@ -1713,6 +1714,243 @@ int moe_backward(const moe_config* cfg, const void* grad_out, float aux_coef, co
                                         T, d, k, E, st),
                      "combine_bwd"));
     trace_mark(st, "combine_bwd");
+    return ok();
+}
+
+// ---------------------------------------------------------------- few tokens, 4-bit weights
+
+static_assert(MOE_FEW_MAX_T == FEW_MAX_T, "token limits differ");
+
+// Workspace of the few-token layer.
+struct FewPlan {
+    Plan P;
+    size_t off_logits, off_table, off_ppart, off_hpart, off_cnt, off_idx, off_gate, off_sums,
+        off_part, total;
+};
+
+static int few_plan_or_fail(const moe_config* cfg, FewPlan* f) {
+    MOE_TRY(plan_or_fail(cfg, &f->P));
+    const Plan& P = f->P;
+    if (!P.bf16) return fail(MOE_ERR_DTYPE, "the few-token layer is bf16 only");
+    if (P.T > FEW_MAX_T)
+        return fail(MOE_ERR_SHAPE, "the few-token layer takes at most %d tokens (T = %lld)",
+                    FEW_MAX_T, (long long)P.T);
+    if (P.reroute) return fail(MOE_ERR_UNSUPPORTED, "the few-token layer: the drop policy only");
+    if (P.train) return fail(MOE_ERR_UNSUPPORTED, "the few-token layer keeps nothing for moe_backward (train = 0)");
+    size_t o = 0;
+    auto take = [&](size_t bytes) { size_t at = o; o = align256(o + bytes); return at; };
+    take(256);  // status words
+    const size_t T = (size_t)P.T, E = (size_t)P.E, k = (size_t)P.k;
+    f->off_logits = take(T * E * 4);
+    f->off_table = take(T * (k + 1) * sizeof(int4));
+    f->off_ppart = take(E * 4);
+    f->off_hpart = take(4);
+    f->off_cnt = take(E * 4);
+    f->off_idx = take(T * k * 4);
+    f->off_gate = take(T * k * 4);
+    f->off_sums = take((2 + 3 * E) * 8);
+    f->off_part = take(P.T ? (size_t)few_part_rows((int)P.T, P.h, P.E, P.k, P.hsum) * P.d * 4 : 0);
+    f->total = o;
+    return MOE_OK;
+}
+
+static int check_group(int32_t group) {
+    if (group != 32 && group != 64 && group != 128)
+        return fail(MOE_ERR_ARG, "group must be 32, 64 or 128");
+    return MOE_OK;
+}
+
+static int few_forward(const moe_config* cfg, int32_t group, const void* x, const float* Wr,
+                       const float* bias, const void* w13, const void* w2, const void* w13s,
+                       const void* w2s, void* out, int32_t* topk_idx, float* topk_gate,
+                       int32_t* routed, int32_t* kept, moe_stats* stats, void* ws,
+                       size_t ws_bytes, void* stream) {
+    FewPlan F;
+    MOE_TRY(few_plan_or_fail(cfg, &F));
+    const Plan& P = F.P;
+    if (!ws) return fail(MOE_ERR_ARG, "ws is NULL");
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return fail(MOE_ERR_ALIGN, "ws is not 256-byte aligned");
+    if (ws_bytes < F.total)
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes; this config needs %zu", ws_bytes,
+                    F.total);
+    MOE_TRY(need(routed, "routed"));
+    MOE_TRY(need(kept, "kept"));
+    MOE_TRY(maybe(stats, "stats"));
+    if (P.T > 0) {
+        MOE_TRY(need(x, "x"));
+        MOE_TRY(need(Wr, "Wr"));
+        MOE_TRY(need(w13, group ? "Q13" : "W13"));
+        MOE_TRY(need(w2, group ? "Q2" : "W2p"));
+        MOE_TRY(need(out, "out"));
+        MOE_TRY(need(topk_idx, "topk_idx"));
+        MOE_TRY(need(topk_gate, "topk_gate"));
+        if (cfg->has_bias) MOE_TRY(need(bias, "bias"));
+        if (P.S > 0) {
+            MOE_TRY(need(w13s, group ? "Q13s" : "W13s"));
+            MOE_TRY(need(w2s, group ? "Q2s" : "W2s"));
+        }
+        if (out == x) return fail(MOE_ERR_ARG, "out must not alias x");
+    }
+    Device dv;
+    MOE_TRY(device_facts(&dv));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    StatsParams sp;
+    sp.ppart = at<float>(ws, F.off_ppart);
+    sp.hpart = at<float>(ws, F.off_hpart);
+    sp.nblk = P.T > 0 ? 1 : 0;
+    sp.routed = routed;
+    sp.kept = kept;
+    sp.T = P.T;
+    sp.E = P.E;
+    sp.k = P.k;
+    sp.sums = at<double>(ws, F.off_sums);
+    sp.stats = stats;
+    if (P.T == 0) {
+        MOE_TRY(empty_batch(P, ws, routed, kept, nullptr, st));
+        if (stats) MOE_TRY(launched(launch_stats(sp, st), "stats"));
+        return ok();
+    }
+    trace_call_begin(st);
+    FewArgs a;
+    memset(&a, 0, sizeof a);
+    a.x = x;
+    a.logits = at<float>(ws, F.off_logits);
+    a.bias = cfg->has_bias ? bias : nullptr;
+    a.w13 = w13;
+    a.w2 = w2;
+    a.w13s = w13s;
+    a.w2s = w2s;
+    a.G = group;
+    a.T = (int)P.T;
+    a.d = P.d;
+    a.h = P.h;
+    a.E = P.E;
+    a.k = P.k;
+    a.hsum = P.hsum;
+    a.C = P.C;
+    a.topk_idx = topk_idx;
+    a.topk_gate = topk_gate;
+    a.routed = routed;
+    a.kept = kept;
+    a.table = at<int4>(ws, F.off_table);
+    a.part = at<float>(ws, F.off_part);
+    a.out = out;
+    a.status = at<int32_t>(ws, 0);
+    a.wait_limit_ns = g_wait_limit_ns;
+    if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return fail(MOE_ERR_CUDA, "memset failed");
+    trace_pre(st, "few_router");
+    MOE_TRY(launched(launch_router_rows(x, true, Wr, at<float>(ws, F.off_logits), a.T, P.d, P.E, st),
+                     "few_router"));
+    trace_mark(st, "few_router");
+    trace_pre(st, "few_ffn");
+    MOE_TRY(launched(launch_few_ffn(a, st), "few_ffn"));
+    trace_mark(st, "few_ffn");
+    trace_pre(st, "few_combine");
+    MOE_TRY(launched(launch_few_combine(a, st), "few_combine"));
+    trace_mark(st, "few_combine");
+    if (stats) {
+        // the full softmax's sums, from the top-k kernel of moe_route on the same
+        // logits (its choices go to scratch: they are the ones above)
+        RouteParams r;
+        memset(&r, 0, sizeof r);
+        r.src = a.logits;
+        r.bias = a.bias;
+        r.zbuf = at<float>(ws, F.off_logits);
+        r.T = P.T;
+        r.E = P.E;
+        r.k = P.k;
+        r.topk_idx = at<int32_t>(ws, F.off_idx);
+        r.topk_gate = at<float>(ws, F.off_gate);
+        r.ppart = at<float>(ws, F.off_ppart);
+        r.hpart = at<float>(ws, F.off_hpart);
+        r.cnt = at<int32_t>(ws, F.off_cnt);
+        r.nsub = 1;
+        r.status = at<int32_t>(ws, 64);  // its own words: it clears them
+        MOE_TRY(launched(launch_topk(r, st), "topk"));
+        MOE_TRY(launched(launch_stats(sp, st), "stats"));
+    }
+    return ok();
+}
+
+int moe_few_workspace_size(const moe_config* cfg, size_t* bytes) {
+    if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
+    FewPlan F;
+    MOE_TRY(few_plan_or_fail(cfg, &F));
+    *bytes = F.total;
+    return ok();
+}
+
+int moe_forward_few(const moe_config* cfg, const void* x, const float* Wr, const float* bias,
+                    const void* W13, const void* W2p, const void* W13s, const void* W2s, void* out,
+                    int32_t* topk_idx, float* topk_gate, int32_t* routed, int32_t* kept,
+                    moe_stats* stats, void* ws, size_t ws_bytes, void* stream) {
+    return few_forward(cfg, 0, x, Wr, bias, W13, W2p, W13s, W2s, out, topk_idx, topk_gate, routed,
+                       kept, stats, ws, ws_bytes, stream);
+}
+
+int moe_forward_few_q4(const moe_config* cfg, int32_t group, const void* x, const float* Wr,
+                       const float* bias, const void* Q13, const void* Q2, const void* Q13s,
+                       const void* Q2s, void* out, int32_t* topk_idx, float* topk_gate,
+                       int32_t* routed, int32_t* kept, moe_stats* stats, void* ws,
+                       size_t ws_bytes, void* stream) {
+    MOE_TRY(check_group(group));
+    return few_forward(cfg, group, x, Wr, bias, Q13, Q2, Q13s, Q2s, out, topk_idx, topk_gate,
+                       routed, kept, stats, ws, ws_bytes, stream);
+}
+
+// Experts, hidden width and checks of one set of 4-bit weights.
+static int q4_set(const moe_config* cfg, int which, int32_t group, Plan* P, int* n, int* hid) {
+    MOE_TRY(plan_or_fail(cfg, P));
+    if (which != 0 && which != 1) return fail(MOE_ERR_ARG, "which must be 0 (routed) or 1 (shared)");
+    if (which == 1 && P->S == 0) return fail(MOE_ERR_ARG, "config has no shared experts");
+    if (!P->bf16) return fail(MOE_ERR_DTYPE, "4-bit weights are made from bf16 weights only");
+    MOE_TRY(check_group(group));
+    *n = which == 0 ? P->E : 1;
+    *hid = which == 0 ? P->h : P->hsum;
+    return MOE_OK;
+}
+
+int moe_q4_size(const moe_config* cfg, int which, int32_t group, size_t* bytes13, size_t* bytes2) {
+    if (!bytes13 || !bytes2) return fail(MOE_ERR_ARG, "bytes13 or bytes2 is NULL");
+    Plan P;
+    int n, hid;
+    MOE_TRY(q4_set(cfg, which, group, &P, &n, &hid));
+    *bytes13 = q13_bytes(n, hid, P.d, group);
+    *bytes2 = q2_bytes(n, hid, P.d, group);
+    return ok();
+}
+
+int moe_q4_quantize(const moe_config* cfg, int which, int32_t group, const void* W13,
+                    const void* W2p, void* Q13, void* Q2, void* stream) {
+    Plan P;
+    int n, hid;
+    MOE_TRY(q4_set(cfg, which, group, &P, &n, &hid));
+    MOE_TRY(need(W13, "W13"));
+    MOE_TRY(need(W2p, "W2p"));
+    MOE_TRY(need(Q13, "Q13"));
+    MOE_TRY(need(Q2, "Q2"));
+    Device dv;
+    MOE_TRY(device_facts(&dv));
+    MOE_TRY(launched(launch_q4_quantize(W13, W2p, Q13, Q2, n, hid, P.d, group,
+                                        reinterpret_cast<cudaStream_t>(stream)),
+                     "q4_quantize"));
+    return ok();
+}
+
+int moe_q4_dequantize(const moe_config* cfg, int which, int32_t group, const void* Q13,
+                      const void* Q2, void* W13, void* W2p, void* stream) {
+    Plan P;
+    int n, hid;
+    MOE_TRY(q4_set(cfg, which, group, &P, &n, &hid));
+    MOE_TRY(need(Q13, "Q13"));
+    MOE_TRY(need(Q2, "Q2"));
+    MOE_TRY(need(W13, "W13"));
+    MOE_TRY(need(W2p, "W2p"));
+    Device dv;
+    MOE_TRY(device_facts(&dv));
+    MOE_TRY(launched(launch_q4_dequantize(Q13, Q2, W13, W2p, n, hid, P.d, group,
+                                          reinterpret_cast<cudaStream_t>(stream)),
+                     "q4_dequantize"));
     return ok();
 }
 

@@ -1,0 +1,93 @@
+// few.h -- host interface of the few-token layer (few.cu) and of the 4-bit
+// expert weights (q4.cu): parameters, layouts and launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int FEW_MAX_T = 16;       // tokens of one call
+constexpr int FEW_CTAS = 148;       // CTAs of the expert kernel (one per SM)
+constexpr int FEW_MAX_ITEMS = FEW_MAX_T * 8 + 1;  // experts one batch can hit, and the shared one
+constexpr int FEW_GRAN = 8;         // hidden units per granule, the unit the CTAs share work in
+constexpr int FEW_HCAP = 512;       // hidden units a part holds in shared memory at most
+
+// ---------------------------------------------------------------- 4-bit layout
+//
+// A set is n experts (the routed ones, or the fused shared one) of hidden width
+// hid and model width d; weights are codes q in [-7, 7] stored as q + 8 and one
+// bf16 scale per group of G along the reduction.  Codes sit in the order in
+// which a warp's lanes take them as A fragments (m16 x k16, lane 4g + t): one
+// 32-bit word holds a lane's eight codes of one k16 step, nibble i (0..3) the
+// first and nibble i + 4 the second element of fragment register i, where
+// registers 0 and 2 are row g, 1 and 3 row g + 8, at k = 2t, 2t + 1 (registers
+// 0, 1) and 2t + 8, 2t + 9 (registers 2, 3).
+//
+// Q13: codes [n][hid/8][d/128][1024 B]: a block is 16 rows (gate rows of hidden
+//      units 8a..8a+7, then their up rows) x 128 of d; inside, [2][32 lanes][4
+//      words], k16 step = 4 * half + word; then the scales
+//      [n][hid/8][d/128][128/G][16 rows] bf16.
+// Q2:  codes [n][d/128][hid/32][8 row tiles][32 lanes][2 words]: 128 rows of d x
+//      32 hidden units, tile i its rows 16i..16i+15, word = k16 step; then the
+//      scales [n][d/128][hid/G][128 rows] bf16.
+__host__ __device__ inline size_t q13_code_bytes(int64_t n, int hid, int d) {
+    return (size_t)n * (hid / 8) * (d / 128) * 1024;
+}
+__host__ __device__ inline size_t q13_bytes(int64_t n, int hid, int d, int G) {
+    return (size_t)n * (hid / 8) * (d / 128) * (1024 + (size_t)(128 / G) * 32);
+}
+__host__ __device__ inline size_t q2_code_bytes(int64_t n, int hid, int d) {
+    return (size_t)n * (d / 128) * (hid / 32) * 2048;
+}
+__host__ __device__ inline size_t q2_bytes(int64_t n, int hid, int d, int G) {
+    return (size_t)n * (d / 128) * ((size_t)(hid / 32) * 2048 + (size_t)(hid / G) * 256);
+}
+
+int launch_q4_quantize(const void* W13, const void* W2p, void* Q13, void* Q2, int n, int hid,
+                       int d, int G, cudaStream_t st);
+int launch_q4_dequantize(const void* Q13, const void* Q2, void* W13, void* W2p, int n, int hid,
+                         int d, int G, cudaStream_t st);
+
+// ---------------------------------------------------------------- the layer
+
+// Parts the experts' hidden units are cut into: `tot` granules in item order
+// (hit experts ascending, then the shared one) over V parts, part v holding
+// [v tot / V, (v + 1) tot / V); every CTA of the grid takes the same number of
+// parts within one, and none holds more than FEW_HCAP hidden units.
+__host__ __device__ inline int few_parts(int64_t tot, int ctas) {
+    const int64_t per = (int64_t)ctas * FEW_HCAP / FEW_GRAN;
+    const int64_t V = ctas * ((tot + per - 1) / per);
+    return (int)(V < tot ? V : tot);
+}
+
+struct FewArgs {
+    const void* x;              // [T][d] bf16
+    const float* logits;        // [T][E] router logits without bias
+    const float* bias;          // [E] or null
+    // routed and shared weights: packed bf16, or codes (scales follow them)
+    const void* w13;
+    const void* w2;
+    const void* w13s;
+    const void* w2s;
+    int G;                      // 0: bf16, else the group of the 4-bit scales
+    int T, d, h, E, k, hsum;
+    int64_t C;                  // capacity
+    int32_t* topk_idx;          // [T][k]
+    float* topk_gate;           // [T][k]
+    int32_t* routed;            // [E]
+    int32_t* kept;              // [E]
+    int4* table;                // [T][k + 1]: first partial row, rows, row stride of each use
+    float* part;                // [rows][d] partial outputs
+    void* out;                  // [T][d] bf16
+    int32_t* status;
+    uint64_t wait_limit_ns;
+};
+
+// Upper bound on the rows of FewArgs::part for any routing of the batch.
+int64_t few_part_rows(int T, int h, int E, int k, int hsum);
+int launch_few_ffn(const FewArgs& a, cudaStream_t st);
+int launch_few_combine(const FewArgs& a, cudaStream_t st);
+
+}  // namespace moe
