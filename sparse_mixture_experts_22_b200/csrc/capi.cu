@@ -1837,13 +1837,21 @@ static int few_forward(const moe_config* cfg, int32_t group, const void* x, cons
     a.out = out;
     a.status = at<int32_t>(ws, 0);
     a.wait_limit_ns = g_wait_limit_ns;
-    if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return fail(MOE_ERR_CUDA, "memset failed");
+    a.test_stall = g_test_stall;
+    CUtensorMap m2, m2s;
+    memset(&m2, 0, sizeof m2);
+    m2s = m2;
+    if (!group) {
+        MOE_TRY(tmap_bf16(&m2, w2, (int64_t)P.E * P.d, P.h, 128));
+        if (P.S > 0) MOE_TRY(tmap_bf16(&m2s, w2s, P.d, P.hsum, 128));
+    }
     trace_pre(st, "few_router");
-    MOE_TRY(launched(launch_router_rows(x, true, Wr, at<float>(ws, F.off_logits), a.T, P.d, P.E, st),
+    MOE_TRY(launched(launch_few_router(x, Wr, at<float>(ws, F.off_logits), a.T, P.d, P.E, a.status,
+                                       st),
                      "few_router"));
     trace_mark(st, "few_router");
     trace_pre(st, "few_ffn");
-    MOE_TRY(launched(launch_few_ffn(a, st), "few_ffn"));
+    MOE_TRY(launched(launch_few_ffn(m2, m2s, a, dv.smem_optin, st), "few_ffn"));
     trace_mark(st, "few_ffn");
     trace_pre(st, "few_combine");
     MOE_TRY(launched(launch_few_combine(a, st), "few_combine"));

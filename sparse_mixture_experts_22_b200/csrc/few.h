@@ -2,6 +2,7 @@
 // expert weights (q4.cu): parameters, layouts and launchers.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -83,11 +84,18 @@ struct FewArgs {
     void* out;                  // [T][d] bf16
     int32_t* status;
     uint64_t wait_limit_ns;
+    int test_stall;             // test hook: block 0 brings nothing in
 };
 
 // Upper bound on the rows of FewArgs::part for any routing of the batch.
 int64_t few_part_rows(int T, int h, int E, int k, int hsum);
-int launch_few_ffn(const FewArgs& a, cudaStream_t st);
+// Logits z [T][E] = x Wr; also clears the status word.
+int launch_few_router(const void* x, const float* Wr, float* z, int T, int d, int E,
+                      int32_t* status, cudaStream_t st);
+// m2, m2s: tensor maps of W2p and W2s as rows of the hidden width, boxes of 64
+// columns x 128 rows with the 128-byte swizzle (bf16 weights; else unused).
+int launch_few_ffn(const CUtensorMap& m2, const CUtensorMap& m2s, const FewArgs& a, int smem_limit,
+                   cudaStream_t st);
 int launch_few_combine(const FewArgs& a, cudaStream_t st);
 
 }  // namespace moe

@@ -335,6 +335,25 @@ def test_prefill_then_decode_from_the_same_4_bits():
         F.check(run(layer, x.cuda()), ref)
 
 
+@pytest.mark.parametrize("group", [0, 64])
+def test_a_wait_that_runs_out_is_reported(group):
+    """The test hook keeps block 0 from bringing anything in: its bounded waits
+    run out, the status says so, and the next call is as before."""
+    wl, inp, ref = made("full", group)
+    layer, g = make_layer(wl, inp, group)
+    want = run(layer, g["x"])["out"].clone()
+    M.moe_set_wait_limit_ns(5_000_000)
+    M.binding.moe_set_test_stall(True)
+    try:
+        layer(g["x"])
+        status = M.moe_read_device_status(layer.ws)
+    finally:
+        M.binding.moe_set_test_stall(False)
+        M.moe_set_wait_limit_ns(2_000_000_000)
+    assert status == 7
+    assert torch.equal(run(layer, g["x"])["out"], want)
+
+
 def test_launch_count_of_a_decode_step():
     wl, inp, _ = made("shared")
     layer, g = make_layer(wl, inp)
