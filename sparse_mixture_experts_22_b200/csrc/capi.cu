@@ -297,6 +297,32 @@ static int tmap_bf16(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols
     return MOE_OK;
 }
 
+// A tensor map of bf16 data with `rank` dimensions (innermost first, contiguous).
+static int tmap_boxes(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
+                      const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    cuuint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr),
+                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return MOE_OK;
+}
+
+// Packed weights of n experts of hidden width hid, as the few-token layer's
+// kernel reads them (FewMaps).
+static int few_maps(CUtensorMap* m13, CUtensorMap* m2, const void* w13, const void* w2, int64_t n,
+                    int hid, int d) {
+    const cuuint64_t d13[3] = {(cuuint64_t)d, 128, (cuuint64_t)(n * 2 * hid / 128)};
+    const cuuint32_t b13[3] = {64, 32, 2};
+    MOE_TRY(tmap_boxes(m13, w13, 3, d13, b13, CU_TENSOR_MAP_SWIZZLE_128B));
+    const cuuint64_t d2[2] = {(cuuint64_t)hid, (cuuint64_t)(n * d)};
+    const cuuint32_t b2[2] = {32, 128};
+    return tmap_boxes(m2, w2, 2, d2, b2, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 // ---------------------------------------------------------------- dependent launch
 
 static int g_pdl_enabled = 1;
@@ -1838,12 +1864,11 @@ static int few_forward(const moe_config* cfg, int32_t group, const void* x, cons
     a.status = at<int32_t>(ws, 0);
     a.wait_limit_ns = g_wait_limit_ns;
     a.test_stall = g_test_stall;
-    CUtensorMap m2, m2s;
-    memset(&m2, 0, sizeof m2);
-    m2s = m2;
+    FewMaps maps;
+    memset(&maps, 0, sizeof maps);
     if (!group) {
-        MOE_TRY(tmap_bf16(&m2, w2, (int64_t)P.E * P.d, P.h, 128));
-        if (P.S > 0) MOE_TRY(tmap_bf16(&m2s, w2s, P.d, P.hsum, 128));
+        MOE_TRY(few_maps(&maps.w13, &maps.w2, w13, w2, P.E, P.h, P.d));
+        if (P.S > 0) MOE_TRY(few_maps(&maps.w13s, &maps.w2s, w13s, w2s, 1, P.hsum, P.d));
     }
     trace_pre(st, "few_router");
     MOE_TRY(launched(launch_few_router(x, Wr, at<float>(ws, F.off_logits), a.T, P.d, P.E, a.status,
@@ -1851,7 +1876,7 @@ static int few_forward(const moe_config* cfg, int32_t group, const void* x, cons
                      "few_router"));
     trace_mark(st, "few_router");
     trace_pre(st, "few_ffn");
-    MOE_TRY(launched(launch_few_ffn(m2, m2s, a, dv.smem_optin, st), "few_ffn"));
+    MOE_TRY(launched(launch_few_ffn(maps, a, dv.smem_optin, st), "few_ffn"));
     trace_mark(st, "few_ffn");
     trace_pre(st, "few_combine");
     MOE_TRY(launched(launch_few_combine(a, st), "few_combine"));

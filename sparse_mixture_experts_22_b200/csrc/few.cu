@@ -230,6 +230,27 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// 3-D tiled bulk tensor load (tma_load_2d_hint's, with a third coordinate).
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c0, int c1, int c2, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One arrive of this thread on bar once its cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -267,84 +288,94 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 
 // ---------------------------------------------------------------- the expert kernel
 //
-// Eight warps multiply what a ninth brings in through a ring of stages (bulk
-// copies, one mbarrier per stage).  Weights are the A operand (16 rows), the
-// tokens of one expert the B operand (8 columns a tile), so one instruction
-// takes 256 weights from registers whatever the number of tokens.
+// Sixteen warps multiply what two others bring in through a ring of stages:
+// one issues the weights' copies (tensor maps for bf16, one bulk copy per stage
+// for 4 bits), the other copies the expert's token rows 16 bytes a lane; both
+// signal the stage's mbarrier.  Weights are the A operand (16 rows), the tokens
+// of one expert the B operand (8 columns a tile), so one instruction takes 256
+// weights from registers whatever the number of tokens.
 //
-// First half, per tile of up to MA granules of one expert: the 16 rows of a
-// granule are the gate and the up rows of its 8 hidden units, so a lane's
-// accumulators hold both for the same unit and token.  KW warps share the
-// columns of a stage (KA); their sums meet in shared memory at the end of d,
-// where H = g silu(a) u is formed in fp32 and stored as two bf16 parts.
-// Second half: w2's rows by the part's columns, 128 rows per 8 warps, against
-// both parts of H; the products of one expert go to the part's own rows of the
-// partial outputs.
+// First half, per granule (32 hidden units): four tiles of 16 rows, the gate and
+// the up rows of 8 units each, so that a lane's accumulators hold both for the
+// same unit and token.  KW warps share the columns of a stage; their sums meet
+// in shared memory at the end of d, where H = g silu(a) u is formed in fp32 and
+// stored as two bf16 parts.  Second half: 256 rows of w2 (16 a warp) by the
+// part's columns against both parts of H; the products of one expert go to the
+// part's own rows of the partial outputs.
 //
-// Shared-memory rows of the copied tiles are pitched by 16 bytes (bf16 rows) or
-// swizzled by the tensor copy (w2), so that ldmatrix meets no bank twice; the
-// 4-bit codes arrive in fragment order and are read as they lie.
+// Copied bf16 tiles are swizzled and token rows pitched by 16 bytes, so that
+// ldmatrix meets no bank twice; 4-bit codes arrive in fragment order and are
+// read as they lie.
 template <int G, int NT>
 struct Shape {
     static constexpr bool Q4 = G > 0;
-    static constexpr int KW = Q4 ? 4 : 8;        // warps along the columns
-    static constexpr int GW = 8 / KW;            // warps along the granules
-    static constexpr int KA = 512;               // columns of a stage
-    static constexpr int MA = Q4 ? (NT == 1 ? 8 : 4) : 2;  // granules of a stage
-    static constexpr int MW = MA / GW;           // granules of a warp
-    static constexpr int XPITCH = KA * 2 + 16;   // bytes of a token's row in a stage
-    static constexpr int WPITCH = KA * 2 + 16;   // bytes of a bf16 weight row
-    static constexpr int SCALES = MA * 4096;     // 4 bits: where a stage's scales begin
-    static constexpr int XOFF = Q4 ? MA * 4608 : MA * 16 * WPITCH;  // where its tokens begin
-    static constexpr int RB = Q4 ? MA / 4 : 2;   // blocks of 128 rows of a down stage
-    static constexpr int HALIGN = Q4 ? 32 : 16;  // H of one expert is padded to this
-    static constexpr int HPITCH = (FEW_HCAP + 64 + 8) * 2;  // bytes of a token's row of H
+    static constexpr int GG = Q4 ? G : 128;
+    static constexpr int KP = Q4 ? 128 : 64;               // columns of a warp in a stage
+    static constexpr int KW = Q4 && NT == 1 ? 8 : 4;       // warps along the columns
+    static constexpr int KA = KW * KP;                     // columns of a stage
+    static constexpr int GW = 16 / KW;                     // warps along the 16-row tiles
+    static constexpr int MW = 4 / GW;                      // tiles of a warp
+    static constexpr int QB = q13_block_bytes(GG);
+    static constexpr int XPITCH = KA * 2 + 16;             // bytes of a token's row in a stage
+    static constexpr int XOFF = Q4 ? KA / 128 * QB : KA * 128;  // where its tokens begin
+    // down: 2 blocks of 128 rows x 8 panels of 32 units (4 bits) or 2 (bf16)
+    static constexpr int PANELS = Q4 ? 8 : 2;
+    static constexpr int SCALES = 32768;                   // 4 bits: where its scales begin
+    static constexpr int GROUPS = GG == 32 ? 8 : 256 / GG + 1;  // groups that 8 panels can meet
+    static constexpr int HPITCH = (FEW_HCAP + 8) * 2;      // bytes of a token's row of H
     static constexpr int HPART = NT * 8 * HPITCH;
-    static constexpr int RED = 8 * MW * NT * 8 * 20 * 4;    // bytes of the warps' sums
+    static constexpr int RED = 16 * MW * NT * 8 * 20 * 4;  // bytes of the warps' sums
     static __host__ __device__ int slot(int T) {
-        const int b = XOFF + T * XPITCH;
-        return (b + 1023) / 1024 * 1024;
+        const int up = XOFF + T * XPITCH, down = Q4 ? SCALES + 2 * GROUPS * 256 : 32768;
+        return ((up > down ? up : down) + 1023) / 1024 * 1024;
     }
     static __host__ __device__ size_t fixed() {
-        return 1024 + 2 * HPART + RED + sizeof(Routing) + 256;
+        return 1024 + 2 * HPART + RED + sizeof(Routing) + 512;
     }
 };
 
 constexpr int MAX_STAGES = 12;
-constexpr int FFN_THREADS = 288;
-constexpr int CONSUMERS = 256;
+constexpr int CONSUMERS = 512;
+constexpr int FFN_THREADS = CONSUMERS + 64;
+constexpr int MAX_SEGS = FEW_HCAP / 128 + 2;  // experts (at least 128 units each) a part can meet
 
 // One expert's share of a part.
 struct Seg {
-    int item, expert, n;   // expert -1: shared
+    int item, expert, n;   // expert -1: shared; tokens
     int j0, len;           // hidden units j0 .. j0 + len
     int row;               // its first row of the partial outputs
-    int hb, front;         // where its H begins; units of padding before j0
-    int64_t next;          // granule after it
+    int hb;                // where its H begins
 };
 
-template <int HALIGN>
-__device__ __forceinline__ Seg segment(const FewArgs& a, const Routing& r, int v, int64_t s0,
-                                       int64_t g1, int hb) {
+// Share i of part v (granules g0 .. g1); false past the last one.
+__device__ __forceinline__ bool segment(const FewArgs& a, const Routing& r, int v, int64_t g0,
+                                        int64_t g1, int i, Seg& s) {
     const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
     const int A = r.items - (gS > 0);
-    Seg s;
-    s.item = (int)min(s0 / gE, (int64_t)A);
+    s.item = (int)min(g0 / gE, (int64_t)A) + i;
+    if (s.item >= r.items) return false;
     const int64_t is = item_start(s.item, A, gE);
-    s.next = min(is + (s.item < A ? gE : gS), g1);
+    const int64_t s0 = max(is, g0), s1 = min(is + (s.item < A ? gE : gS), g1);
+    if (s0 >= s1) return false;
     s.expert = r.expert[s.item];
     s.n = r.n[s.item];
     s.j0 = (int)(s0 - is) * FEW_GRAN;
-    s.len = (int)(s.next - s0) * FEW_GRAN;
+    s.len = (int)(s1 - s0) * FEW_GRAN;
     s.row = r.row0[s.item] + (v - part_of(is, r.tot, r.V)) * s.n;
-    s.hb = hb;
-    s.front = HALIGN == 32 ? s.j0 % 32 : 0;
-    return s;
+    s.hb = (int)(s0 - g0) * FEW_GRAN;
+    return true;
 }
 
-template <int HALIGN>
-__device__ __forceinline__ int padded(const Seg& s) {
-    return (s.front + s.len + HALIGN - 1) / HALIGN * HALIGN;
+// A warp writes part v's shares to segs; returns how many there are.
+__device__ __forceinline__ int segments(const FewArgs& a, const Routing& r, int v, Seg* segs) {
+    const int lane = threadIdx.x & 31;
+    const int64_t g0 = (int64_t)v * r.tot / r.V, g1 = (int64_t)(v + 1) * r.tot / r.V;
+    Seg s;
+    const bool have = lane < MAX_SEGS && segment(a, r, v, g0, g1, lane, s);
+    __syncwarp();
+    if (have) segs[lane] = s;
+    __syncwarp();
+    return __popc(__ballot_sync(0xffffffffu, have));
 }
 
 // A ring position: stage and the parity of its current phase.
@@ -359,14 +390,36 @@ struct Ring {
     }
 };
 
+// Calls up(seg, unit, k0) for every stage of the first half and
+// down(seg, r0, p0, np) for every stage of the second (r0 the first of up to 256
+// rows of d, np panels of 32 units from panel p0 of the share) of all parts of
+// this block, in ring order; a call that returns false ends it.
+template <int G, int NT, typename Up, typename Down>
+__device__ __forceinline__ void for_stages(const FewArgs& a, const Routing& r, Seg* segs, Up up,
+                                           Down down) {
+    using S = Shape<G, NT>;
+    for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
+        const int n = segments(a, r, v, segs);
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < segs[i].len; j += FEW_GRAN)
+                for (int k0 = 0; k0 < a.d; k0 += S::KA)
+                    if (!up(segs[i], segs[i].j0 + j, k0)) return;
+        for (int r0 = 0; r0 < a.d; r0 += 256)
+            for (int i = 0; i < n; ++i)
+                for (int p = 0; p < segs[i].len / 32; p += S::PANELS)
+                    if (!down(segs[i], r0, p, min(S::PANELS, segs[i].len / 32 - p))) return;
+    }
+}
+
+// The weights' copies.
 template <int G, int NT>
-__device__ void produce(const FewArgs& a, const Routing& r, const CUtensorMap* m2,
-                        const CUtensorMap* m2s, uint8_t* ring, int slot, int stages,
-                        uint64_t* full, uint64_t* empty, int32_t* issued) {
+__device__ void bring_weights(const FewArgs& a, const Routing& r, const FewMaps& maps, Seg* segs,
+                              uint8_t* ring, int slot, int stages, uint64_t* full,
+                              uint64_t* empty, int32_t* issued) {
     using S = Shape<G, NT>;
     const int lane = threadIdx.x & 31;
     const int d = a.d;
-    const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_normal();
+    const uint64_t once = l2_policy_evict_first();
     Ring p;
     p.stages = stages;
     int count = 0;
@@ -384,102 +437,99 @@ __device__ void produce(const FewArgs& a, const Routing& r, const CUtensorMap* m
         __syncwarp();
         return true;
     };
-    if (a.test_stall && blockIdx.x == 0) return;
-    for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
-        const int64_t g0 = (int64_t)v * r.tot / r.V, g1 = (int64_t)(v + 1) * r.tot / r.V;
-        for (int64_t s0 = g0; s0 < g1;) {
-            const Seg s = segment<S::HALIGN>(a, r, v, s0, g1, 0);
-            s0 = s.next;
-            const bool shared = s.expert < 0;
-            const int hid = shared ? a.hsum : a.h;
-            const int64_t e = shared ? 0 : s.expert;
+    auto up = [&](const Seg& s, int j, int k0) -> bool {
+        const bool shared = s.expert < 0;
+        const int hid = shared ? a.hsum : a.h, e = shared ? 0 : s.expert;
+        const int kn = min(S::KA, d - k0);
+        uint8_t* dst = ring + (size_t)p.stage * slot;
+        if (!open(S::Q4 ? kn / 128 * S::QB : kn * 128)) return false;
+        if (S::Q4) {
             const uint8_t* W = reinterpret_cast<const uint8_t*>(shared ? a.w13s : a.w13);
-            const uint8_t* sc = S::Q4 ? W + q13_code_bytes(shared ? 1 : a.E, hid, d) : nullptr;
-            const int ng = s.len / FEW_GRAN, tiles = (ng + S::MA - 1) / S::MA;
-            for (int tl = 0; tl < tiles; ++tl) {
-                const int t0 = tl * ng / tiles, m = (tl + 1) * ng / tiles - t0;
-                const int j = s.j0 + t0 * FEW_GRAN;
-                for (int k0 = 0; k0 < d; k0 += S::KA) {
-                    const int kn = min(S::KA, d - k0);
-                    const uint32_t wb = S::Q4 ? kn / 128 * (1024 + 32 * (128 / (G ? G : 128)))
-                                              : 16 * kn * 2;
-                    if (!open(m * wb + s.n * kn * 2)) return;
-                    const uint32_t dst = smem_addr(ring + (size_t)p.stage * slot);
-                    if (S::Q4) {
-                        constexpr int SB = 32 * (128 / (G ? G : 128));  // scale bytes of a block
-                        const int g = lane & 7;
-                        const int64_t blk = (e * (hid / 8) + j / 8 + g) * (d / 128) + k0 / 128;
-                        if (g < m && lane < 8)
-                            bulk_load(dst + g * 4096, W + blk * 1024, kn * 8, &full[p.stage], once);
-                        if (g < m && lane >= 8 && lane < 16)
-                            bulk_load(dst + S::SCALES + g * 4 * SB, sc + blk * SB, kn / 128 * SB,
-                                      &full[p.stage], once);
-                        if (lane >= 16 && lane - 16 < s.n)
-                            bulk_load(dst + S::XOFF + (lane - 16) * S::XPITCH,
-                                      reinterpret_cast<const __nv_bfloat16*>(a.x) +
-                                          (int64_t)r.tok[s.item][lane - 16] * d + k0,
-                                      kn * 2, &full[p.stage], keep);
-                    } else {
-                        const int g = lane >> 4, rr = lane & 15, jj = j + g * FEW_GRAN + (rr & 7);
-                        const int64_t row = e * 2 * hid + 256 * (jj / 128) + 128 * (rr >> 3) + jj % 128;
-                        if (g < m)
-                            bulk_load(dst + (g * 16 + rr) * S::WPITCH, W + (row * d + k0) * 2, kn * 2,
-                                      &full[p.stage], once);
-                        if (lane < s.n)
-                            bulk_load(dst + S::XOFF + lane * S::XPITCH,
-                                      reinterpret_cast<const __nv_bfloat16*>(a.x) +
-                                          (int64_t)r.tok[s.item][lane] * d + k0,
-                                      kn * 2, &full[p.stage], keep);
-                    }
-                    p.next();
-                }
-            }
+            const int64_t blk = ((int64_t)e * (hid / 32) + j / 32) * (d / 128) + k0 / 128;
+            if (lane == 0)
+                bulk_load(smem_addr(dst), W + blk * S::QB, kn / 128 * S::QB, &full[p.stage], once);
+        } else if (lane < kn / 64) {
+            tma_load_3d_hint(dst + lane * 8192, shared ? &maps.w13s : &maps.w13, &full[p.stage],
+                             k0 + lane * 64, j % 128, 2 * (int)(((int64_t)e * hid + j) / 128), once);
         }
-        for (int r0 = 0; r0 < d; r0 += 128 * S::RB) {
-            const int nb = min(S::RB, (d - r0) / 128);
-            for (int64_t s0 = g0; s0 < g1;) {
-                const Seg s = segment<S::HALIGN>(a, r, v, s0, g1, 0);
-                s0 = s.next;
-                const bool shared = s.expert < 0;
-                const int hid = shared ? a.hsum : a.h;
-                const int64_t e = shared ? 0 : s.expert;
-                if (S::Q4) {
-                    constexpr int GG = G ? G : 128;
-                    const uint8_t* W = reinterpret_cast<const uint8_t*>(shared ? a.w2s : a.w2);
-                    const uint8_t* sc = W + q2_code_bytes(shared ? 1 : a.E, hid, d);
-                    const int p0 = s.j0 / 32, p1 = (s.j0 + s.len + 31) / 32;
-                    for (int pp = p0; pp < p1; pp += 8) {
-                        const int np = min(8, p1 - pp);
-                        const int q0 = pp * 32 / GG, nq = ((pp + np) * 32 - 1) / GG - q0 + 1;
-                        if (!open(nb * (np * 2048 + nq * 256))) return;
-                        const uint32_t dst = smem_addr(ring + (size_t)p.stage * slot);
-                        if (lane < nb) {
-                            const int64_t rb = e * (d / 128) + r0 / 128 + lane;
-                            bulk_load(dst + lane * 16384, W + (rb * (hid / 32) + pp) * 2048, np * 2048,
-                                      &full[p.stage], once);
-                            bulk_load(dst + S::SCALES + lane * 2048, sc + (rb * (hid / GG) + q0) * 256,
-                                      nq * 256, &full[p.stage], once);
-                        }
-                        p.next();
-                    }
-                } else {
-                    for (int c = 0; c < s.len; c += 64) {
-                        if (!open(nb * 16384)) return;
-                        if (lane < nb)
-                            tma_load_2d_hint(ring + (size_t)p.stage * slot + lane * 16384,
-                                             shared ? m2s : m2, &full[p.stage], s.j0 + c,
-                                             (int)(e * d + r0 + 128 * lane), once);
-                        p.next();
-                    }
-                }
-            }
+        p.next();
+        return true;
+    };
+    auto down = [&](const Seg& s, int r0, int p0, int np) -> bool {
+        const bool shared = s.expert < 0;
+        const int hid = shared ? a.hsum : a.h, e = shared ? 0 : s.expert;
+        const int nb = min(2, (d - r0) / 128);
+        uint8_t* dst = ring + (size_t)p.stage * slot;
+        if (S::Q4) {
+            const uint8_t* W = reinterpret_cast<const uint8_t*>(shared ? a.w2s : a.w2);
+            const uint8_t* sc = W + q2_code_bytes(shared ? 1 : a.E, hid, d);
+            const int pp = s.j0 / 32 + p0;
+            const int q0 = pp * 32 / S::GG, nq = ((pp + np) * 32 - 1) / S::GG - q0 + 1;
+            if (!open(nb * (np * 2048 + nq * 256))) return false;
+            const int b = lane & 1;
+            const int64_t rb = (int64_t)e * (d / 128) + r0 / 128 + b;
+            if (b < nb && lane < 2)
+                bulk_load(smem_addr(dst) + b * 16384, W + (rb * (hid / 32) + pp) * 2048, np * 2048,
+                          &full[p.stage], once);
+            if (b < nb && (lane >> 1) == 1)
+                bulk_load(smem_addr(dst) + S::SCALES + b * S::GROUPS * 256,
+                          sc + (rb * (hid / S::GG) + q0) * 256, nq * 256, &full[p.stage], once);
+        } else {
+            if (!open(nb * np * 8192)) return false;
+            const int b = lane & 1, c = lane >> 1;
+            if (b < nb && c < np)
+                tma_load_2d_hint(dst + lane * 8192, shared ? &maps.w2s : &maps.w2, &full[p.stage],
+                                 s.j0 + (p0 + c) * 32, e * d + r0 + 128 * b, once);
         }
-    }
+        p.next();
+        return true;
+    };
+    for_stages<G, NT>(a, r, segs, up, down);
+}
+
+// The token rows of the first half, 16 bytes a lane; every lane arrives on
+// every stage, when its copies have landed.
+template <int G, int NT>
+__device__ void bring_tokens(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring,
+                             int slot, int stages, uint64_t* full, uint64_t* empty) {
+    using S = Shape<G, NT>;
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(a.x);
+    Ring p;
+    p.stages = stages;
+    auto open = [&]() -> bool {
+        const bool ok = mbar_wait(&empty[p.stage], p.phase ^ 1, a.wait_limit_ns);
+        return __all_sync(0xffffffffu, ok);
+    };
+    auto up = [&](const Seg& s, int, int k0) -> bool {
+        if (!open()) return false;
+        const int vecs = min(S::KA, a.d - k0) / 8;
+        const uint32_t dst = smem_addr(ring + (size_t)p.stage * slot) + S::XOFF;
+        for (int n = 0; n < s.n; ++n) {
+            const __nv_bfloat16* src = x + (int64_t)r.tok[s.item][n] * a.d + k0;
+#pragma unroll
+            for (int q = 0; q < S::KA / 256; ++q)
+                if (q * 32 + lane < vecs)
+                    cp_async16(dst + n * S::XPITCH + (q * 32 + lane) * 16, src + (q * 32 + lane) * 8);
+        }
+        cp_async_arrive(&full[p.stage]);
+        p.next();
+        return true;
+    };
+    auto down = [&](const Seg&, int, int, int) -> bool {
+        if (!open()) return false;
+        mbar_arrive(&full[p.stage]);
+        p.next();
+        return true;
+    };
+    for_stages<G, NT>(a, r, segs, up, down);
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int G, int NT>
-__device__ void consume(const FewArgs& a, const Routing& r, uint8_t* ring, int slot, int stages,
-                        uint64_t* full, uint64_t* empty, uint8_t* Hs, float* red, int32_t* dead) {
+__device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring, int slot,
+                        int stages, uint64_t* full, uint64_t* empty, uint8_t* Hs, float* red,
+                        int32_t* flags) {
     using S = Shape<G, NT>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int kw = warp % S::KW, gw = warp / S::KW;
@@ -493,7 +543,7 @@ __device__ void consume(const FewArgs& a, const Routing& r, uint8_t* ring, int s
     auto wait = [&]() -> uint32_t {
         if (!lost && !mbar_wait(&full[p.stage], p.phase, a.wait_limit_ns)) {
             lost = true;
-            *dead = 1;
+            flags[0] = 1;
             report_timeout(a.status);
         }
         lost = __any_sync(0xffffffffu, lost);
@@ -505,107 +555,111 @@ __device__ void consume(const FewArgs& a, const Routing& r, uint8_t* ring, int s
         p.next();
     };
     for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
-        const int64_t g0 = (int64_t)v * r.tot / r.V, g1 = (int64_t)(v + 1) * r.tot / r.V;
+        named_sync(1, CONSUMERS);  // the last part's shares and H have been read
+        if (warp == 0) {
+            const int n = segments(a, r, v, segs);
+            if (lane == 0) flags[2] = n;
+        }
+        named_sync(1, CONSUMERS);
+        const int nseg = flags[2];
         // ---------------------------------------------------- H
-        int hb = 0;
-        for (int64_t s0 = g0; s0 < g1;) {
-            const Seg s = segment<S::HALIGN>(a, r, v, s0, g1, hb);
-            s0 = s.next;
-            hb += padded<S::HALIGN>(s);
-            const int ng = s.len / FEW_GRAN, tiles = (ng + S::MA - 1) / S::MA;
+        for (int i = 0; i < nseg; ++i) {
+            const Seg s = segs[i];
             // rows of tokens past the expert's repeat its last one: their columns
             // of the product are never read
             uint32_t xrow[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                xrow[nt] = S::XOFF + min(nt * 8 + lm, s.n - 1) * S::XPITCH;
-            for (int tl = 0; tl < tiles; ++tl) {
-                const int t0 = tl * ng / tiles, m = (tl + 1) * ng / tiles - t0;
+                xrow[nt] = S::XOFF + min(nt * 8 + lm, s.n - 1) * S::XPITCH +
+                           (kw * S::KP + lq * 8) * 2;
+            for (int j = 0; j < s.len; j += FEW_GRAN) {
                 float acc[S::MW][NT][4];
 #pragma unroll
-                for (int i = 0; i < S::MW; ++i)
+                for (int m = 0; m < S::MW; ++m)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[i][nt][q] = 0.f;
+                        for (int q = 0; q < 4; ++q) acc[m][nt][q] = 0.f;
                 for (int k0 = 0; k0 < d; k0 += S::KA) {
                     const uint32_t st = wait();
-                    constexpr int KP = S::KA / S::KW;  // columns of a warp
-                    if (!lost && k0 + kw * KP < d) {
+                    if (!lost && k0 + kw * S::KP < d) {
+                        uint32_t b[NT][S::KP / 32][4];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (nt * 8 >= s.n) break;
-                            uint32_t b[KP / 32][4];
+                        for (int nt = 0; nt < NT; ++nt)
+                            if (nt * 8 < s.n) {
 #pragma unroll
-                            for (int q = 0; q < KP / 32; ++q)
-                                ldmatrix4(st + xrow[nt] + (kw * KP + q * 32 + lq * 8) * 2, b[q]);
+                                for (int q = 0; q < S::KP / 32; ++q)
+                                    ldmatrix4(st + xrow[nt] + q * 64, b[nt][q]);
+                            }
+#pragma unroll
+                        for (int m = 0; m < S::MW; ++m) {
+                            const int g = m * S::GW + gw;
                             if (S::Q4) {
-                                constexpr int GG = G ? G : 128, SB = 32 * (128 / GG);
+                                const uint4* cw = reinterpret_cast<const uint4*>(
+                                    ring + (size_t)p.stage * slot + kw * S::QB + g * 1024);
+                                uint32_t w[8];
+                                *reinterpret_cast<uint4*>(w) = cw[lane];
+                                *reinterpret_cast<uint4*>(w + 4) = cw[32 + lane];
+                                const uint32_t sa = st + kw * S::QB + 4096 + (g * 16 + fg) * 2;
 #pragma unroll
-                                for (int i = 0; i < S::MW; ++i) {
-                                    const int g = i * S::GW + gw;
-                                    if (g >= m) break;
-                                    uint32_t w[8];
-                                    const uint4* cw = reinterpret_cast<const uint4*>(
-                                        ring + (size_t)p.stage * slot + g * 4096 + kw * 1024);
-                                    *reinterpret_cast<uint4*>(w) = cw[lane];
-                                    *reinterpret_cast<uint4*>(w + 4) = cw[32 + lane];
-                                    const uint32_t sa = st + S::SCALES + (g * 4 + kw) * SB + fg * 2;
+                                for (int q = 0; q < 128 / S::GG; ++q) {
+                                    float c[NT][4];
 #pragma unroll
-                                    for (int q = 0; q < 128 / GG; ++q) {
-                                        float c[4] = {0.f, 0.f, 0.f, 0.f};
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
 #pragma unroll
-                                        for (int u = 0; u < GG / 16; ++u) {
-                                            const int k16 = q * (GG / 16) + u;
-                                            uint32_t f[4];
-                                            codes_to_frag(w[k16], f);
-                                            mma(c, f, b[k16 / 2][2 * (k16 & 1)],
-                                                b[k16 / 2][2 * (k16 & 1) + 1]);
-                                        }
-                                        const float sl = lds_bf16(sa + q * 32);
-                                        const float sh = lds_bf16(sa + q * 32 + 16);
-                                        acc[i][nt][0] = fmaf(c[0], sl, acc[i][nt][0]);
-                                        acc[i][nt][1] = fmaf(c[1], sl, acc[i][nt][1]);
-                                        acc[i][nt][2] = fmaf(c[2], sh, acc[i][nt][2]);
-                                        acc[i][nt][3] = fmaf(c[3], sh, acc[i][nt][3]);
+                                    for (int u = q * (S::GG / 16); u < (q + 1) * (S::GG / 16); ++u) {
+                                        uint32_t f[4];
+                                        codes_to_frag(w[u], f);
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt)
+                                            if (nt * 8 < s.n)
+                                                mma(c[nt], f, b[nt][u / 2][2 * (u & 1)],
+                                                    b[nt][u / 2][2 * (u & 1) + 1]);
+                                    }
+                                    const float sl = lds_bf16(sa + q * 128);
+                                    const float sh = lds_bf16(sa + q * 128 + 16);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        acc[m][nt][0] = fmaf(c[nt][0], sl, acc[m][nt][0]);
+                                        acc[m][nt][1] = fmaf(c[nt][1], sl, acc[m][nt][1]);
+                                        acc[m][nt][2] = fmaf(c[nt][2], sh, acc[m][nt][2]);
+                                        acc[m][nt][3] = fmaf(c[nt][3], sh, acc[m][nt][3]);
                                     }
                                 }
                             } else {
+                                // box of this warp's 64 columns: 32 gate rows, 32 up rows
+                                const uint32_t wa = st + kw * 8192 + ((lq & 1) * 32 + g * 8 + lm) * 128;
 #pragma unroll
-                                for (int i = 0; i < S::MW; ++i) {
-                                    if (i >= m) break;
-                                    const uint32_t wa =
-                                        st + (i * 16 + (lq & 1) * 8 + lm) * S::WPITCH +
-                                        (kw * KP + (lq >> 1) * 8) * 2;
+                                for (int u = 0; u < S::KP / 16; ++u) {
+                                    uint32_t f[4];
+                                    ldmatrix4(wa + (((u * 2 + (lq >> 1)) ^ lm) << 4), f);
 #pragma unroll
-                                    for (int u = 0; u < KP / 16; ++u) {
-                                        uint32_t f[4];
-                                        ldmatrix4(wa + u * 32, f);
-                                        mma(acc[i][nt], f, b[u / 2][2 * (u & 1)],
-                                            b[u / 2][2 * (u & 1) + 1]);
-                                    }
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        if (nt * 8 < s.n)
+                                            mma(acc[m][nt], f, b[nt][u / 2][2 * (u & 1)],
+                                                b[nt][u / 2][2 * (u & 1) + 1]);
                                 }
                             }
                         }
                     }
                     done();
                 }
-                named_sync(1, CONSUMERS);  // the last tile's sums have been read
+                named_sync(1, CONSUMERS);  // the last granule's sums have been read
 #pragma unroll
-                for (int i = 0; i < S::MW; ++i)
+                for (int m = 0; m < S::MW; ++m)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float* q = red + ((warp * S::MW + i) * NT + nt) * 160 + 2 * ft * 20 + fg;
-                        q[0] = acc[i][nt][0];
-                        q[20] = acc[i][nt][1];
-                        q[8] = acc[i][nt][2];
-                        q[28] = acc[i][nt][3];
+                        float* q = red + ((warp * S::MW + m) * NT + nt) * 160 + 2 * ft * 20 + fg;
+                        q[0] = acc[m][nt][0];
+                        q[20] = acc[m][nt][1];
+                        q[8] = acc[m][nt][2];
+                        q[28] = acc[m][nt][3];
                     }
                 named_sync(1, CONSUMERS);
                 __nv_bfloat16* H = reinterpret_cast<__nv_bfloat16*>(Hs);
-                constexpr int HP = S::HPITCH / 2, HLO = S::HPART / 2;
-                for (int i = tid; i < 8 * m * s.n; i += CONSUMERS) {
-                    const int jj = i & 7, g = (i >> 3) % m, n = (i >> 3) / m;
+                if (tid < FEW_GRAN * s.n) {
+                    const int jj = tid & 7, g = (tid >> 3) & 3, n = tid >> 5;
                     float ga = 0.f, up = 0.f;
 #pragma unroll
                     for (int w = 0; w < S::KW; ++w) {
@@ -616,132 +670,102 @@ __device__ void consume(const FewArgs& a, const Routing& r, uint8_t* ring, int s
                     }
                     const float hv = silu_f(ga) * up * r.gate[s.item][n];
                     const float hi = bf16_round(hv);
-                    const int at = n * HP + s.hb + s.front + (t0 + g) * FEW_GRAN + jj;
+                    const int at = n * (S::HPITCH / 2) + s.hb + j + g * 8 + jj;
                     H[at] = __float2bfloat16_rn(hi);
-                    H[HLO + at] = __float2bfloat16_rn(hv - hi);
-                }
-                if (tl == 0) {  // zeros in the padding on both sides of the expert's units
-                    const int pad = padded<S::HALIGN>(s) - s.len;
-                    for (int i = tid; i < pad * s.n; i += CONSUMERS) {
-                        const int q = i % pad, n = i / pad;
-                        const int at = n * HP + s.hb + (q < s.front ? q : s.len + q);
-                        H[at] = __float2bfloat16_rn(0.f);
-                        H[HLO + at] = __float2bfloat16_rn(0.f);
-                    }
+                    H[S::HPART / 2 + at] = __float2bfloat16_rn(hv - hi);
                 }
             }
         }
         named_sync(1, CONSUMERS);
         // ---------------------------------------------------- this part of the output
-        for (int r0 = 0; r0 < d; r0 += 128 * S::RB) {
-            const int nb = min(S::RB, (d - r0) / 128);
-            hb = 0;
-            for (int64_t s0 = g0; s0 < g1;) {
-                const Seg s = segment<S::HALIGN>(a, r, v, s0, g1, hb);
-                s0 = s.next;
-                hb += padded<S::HALIGN>(s);
-                float acc[S::RB][NT][4];
+        const int rb = warp >> 3, tile = warp & 7;  // this warp's 16 rows of 256
+        for (int r0 = 0; r0 < d; r0 += 256) {
+            const bool mine = r0 + rb * 128 < d;
+            for (int i = 0; i < nseg; ++i) {
+                const Seg s = segs[i];
+                // one chain of products for each part of H
+                float acc[NT][4], low[NT][4];
 #pragma unroll
-                for (int i = 0; i < S::RB; ++i)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[i][nt][q] = 0.f;
+                    for (int q = 0; q < 4; ++q) acc[nt][q] = low[nt][q] = 0.f;
                 // H fragments: matrices (high, k), (high, k + 8), (low, k), (low, k + 8)
                 uint32_t hrow[NT];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     hrow[nt] = hs + (lq >> 1) * S::HPART + min(nt * 8 + lm, s.n - 1) * S::HPITCH +
                                (s.hb + (lq & 1) * 8) * 2;
-                if (S::Q4) {
-                    constexpr int GG = G ? G : 128;
-                    const int p0 = s.j0 / 32, p1 = (s.j0 + s.len + 31) / 32;
-                    for (int pp = p0; pp < p1; pp += 8) {
-                        const int np = min(8, p1 - pp), q0 = pp * 32 / GG;
-                        const uint32_t st = wait();
-                        if (!lost) {
-                            for (int i = 0; i < np; ++i) {
-                                const int gq = (pp + i) * 32 / GG - q0;
+                for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
+                    const int np = min(S::PANELS, s.len / 32 - p0);
+                    const uint32_t st = wait();
+                    if (!lost && mine) {
+                        const int pp = s.j0 / 32 + p0, q0 = pp * 32 / S::GG;
+#pragma unroll 2
+                        for (int c = 0; c < np; ++c) {
+                            uint32_t b[NT][2][4];
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    if (nt * 8 >= s.n) break;
-                                    uint32_t b0[4], b1[4];
-                                    ldmatrix4(hrow[nt] + (pp - p0 + i) * 64, b0);
-                                    ldmatrix4(hrow[nt] + (pp - p0 + i) * 64 + 32, b1);
+                            for (int nt = 0; nt < NT; ++nt)
+                                if (nt * 8 < s.n) {
+                                    ldmatrix4(hrow[nt] + (p0 + c) * 64, b[nt][0]);
+                                    ldmatrix4(hrow[nt] + (p0 + c) * 64 + 32, b[nt][1]);
+                                }
+                            if (S::Q4) {
+                                const uint2 w = reinterpret_cast<const uint2*>(
+                                    ring + (size_t)p.stage * slot + rb * 16384 +
+                                    (c * 8 + tile) * 256)[lane];
+                                const uint32_t sa = st + S::SCALES +
+                                                    (rb * S::GROUPS + (pp + c) * 32 / S::GG - q0) * 256 +
+                                                    (tile * 16 + fg) * 2;
+                                const float sl = lds_bf16(sa), sh = lds_bf16(sa + 16);
+                                uint32_t f0[4], f1[4];
+                                codes_to_frag(w.x, f0);
+                                codes_to_frag(w.y, f1);
 #pragma unroll
-                                    for (int rb = 0; rb < S::RB; ++rb) {
-                                        if (rb >= nb) break;
-                                        const uint2 w = reinterpret_cast<const uint2*>(
-                                            ring + (size_t)p.stage * slot + rb * 16384 +
-                                            (i * 8 + warp) * 256)[lane];
-                                        float c[4] = {0.f, 0.f, 0.f, 0.f};
-                                        uint32_t f[4];
-                                        codes_to_frag(w.x, f);
-                                        mma(c, f, b0[0], b0[1]);
-                                        mma(c, f, b0[2], b0[3]);
-                                        codes_to_frag(w.y, f);
-                                        mma(c, f, b1[0], b1[1]);
-                                        mma(c, f, b1[2], b1[3]);
-                                        const uint32_t sa = st + S::SCALES + rb * 2048 + gq * 256 +
-                                                            (warp * 16 + fg) * 2;
-                                        const float sl = lds_bf16(sa), sh = lds_bf16(sa + 16);
-                                        acc[rb][nt][0] = fmaf(c[0], sl, acc[rb][nt][0]);
-                                        acc[rb][nt][1] = fmaf(c[1], sl, acc[rb][nt][1]);
-                                        acc[rb][nt][2] = fmaf(c[2], sh, acc[rb][nt][2]);
-                                        acc[rb][nt][3] = fmaf(c[3], sh, acc[rb][nt][3]);
+                                for (int nt = 0; nt < NT; ++nt)
+                                    if (nt * 8 < s.n) {
+                                        float ch[4] = {0.f, 0.f, 0.f, 0.f};
+                                        float cl[4] = {0.f, 0.f, 0.f, 0.f};
+                                        mma(ch, f0, b[nt][0][0], b[nt][0][1]);
+                                        mma(cl, f0, b[nt][0][2], b[nt][0][3]);
+                                        mma(ch, f1, b[nt][1][0], b[nt][1][1]);
+                                        mma(cl, f1, b[nt][1][2], b[nt][1][3]);
+                                        acc[nt][0] = fmaf(ch[0] + cl[0], sl, acc[nt][0]);
+                                        acc[nt][1] = fmaf(ch[1] + cl[1], sl, acc[nt][1]);
+                                        acc[nt][2] = fmaf(ch[2] + cl[2], sh, acc[nt][2]);
+                                        acc[nt][3] = fmaf(ch[3] + cl[3], sh, acc[nt][3]);
                                     }
+                            } else {
+                                // box (c, rb): 128 rows of 64 bytes
+                                const int row = tile * 16 + (lq & 1) * 8 + lm;
+                                const uint32_t wa = st + (c * 2 + rb) * 8192 + row * 64;
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    uint32_t f[4];
+                                    ldmatrix4(wa + (((u * 2 + (lq >> 1)) ^ ((lm >> 1) & 3)) << 4), f);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        if (nt * 8 < s.n) {
+                                            mma(acc[nt], f, b[nt][u][0], b[nt][u][1]);
+                                            mma(low[nt], f, b[nt][u][2], b[nt][u][3]);
+                                        }
                                 }
                             }
                         }
-                        done();
                     }
-                } else {
-                    for (int c0 = 0; c0 < s.len; c0 += 64) {
-                        const uint32_t st = wait();
-                        if (!lost) {
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                if (c0 + u * 16 >= s.len) break;
-                                uint32_t f[S::RB][4];
-#pragma unroll
-                                for (int rb = 0; rb < S::RB; ++rb) {
-                                    if (rb >= nb) break;
-                                    const int row = warp * 16 + (lq & 1) * 8 + lm;
-                                    ldmatrix4(st + rb * 16384 + row * 128 +
-                                                  (((u * 2 + (lq >> 1)) ^ lm) << 4),
-                                              f[rb]);
-                                }
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    if (nt * 8 >= s.n) break;
-                                    uint32_t b[4];
-                                    ldmatrix4(hrow[nt] + (c0 + u * 16) * 2, b);
-#pragma unroll
-                                    for (int rb = 0; rb < S::RB; ++rb) {
-                                        if (rb >= nb) break;
-                                        mma(acc[rb][nt], f[rb], b[0], b[1]);
-                                        mma(acc[rb][nt], f[rb], b[2], b[3]);
-                                    }
-                                }
-                            }
-                        }
-                        done();
-                    }
+                    done();
                 }
-#pragma unroll
-                for (int rb = 0; rb < S::RB; ++rb) {
-                    if (rb >= nb) break;
+                if (mine) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const int n = nt * 8 + 2 * ft;
-                        float* q = a.part + (int64_t)(s.row + n) * d + r0 + rb * 128 + warp * 16 + fg;
+                        float* q = a.part + (int64_t)(s.row + n) * d + r0 + rb * 128 + tile * 16 + fg;
                         if (n < s.n) {
-                            q[0] = acc[rb][nt][0];
-                            q[8] = acc[rb][nt][2];
+                            q[0] = acc[nt][0] + low[nt][0];
+                            q[8] = acc[nt][2] + low[nt][2];
                         }
                         if (n + 1 < s.n) {
-                            q[d] = acc[rb][nt][1];
-                            q[d + 8] = acc[rb][nt][3];
+                            q[d] = acc[nt][1] + low[nt][1];
+                            q[d + 8] = acc[nt][3] + low[nt][3];
                         }
                     }
                 }
@@ -752,8 +776,8 @@ __device__ void consume(const FewArgs& a, const Routing& r, uint8_t* ring, int s
 
 template <int G, int NT>
 __global__ void __launch_bounds__(FFN_THREADS, 1)
-    few_ffn_kernel(const __grid_constant__ CUtensorMap m2, const __grid_constant__ CUtensorMap m2s,
-                   const __grid_constant__ FewArgs a, int slot, int stages) {
+    few_ffn_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a,
+                   int slot, int stages) {
     using S = Shape<G, NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + (-smem_addr(smem_raw) & 1023);
@@ -763,27 +787,33 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(
         reinterpret_cast<uint8_t*>(&r) + (sizeof(Routing) + 15) / 16 * 16);
     uint64_t* empty = full + MAX_STAGES;
-    int32_t* flags = reinterpret_cast<int32_t*>(empty + MAX_STAGES);  // dead, issued stages
-    const int tid = threadIdx.x;
+    int32_t* flags = reinterpret_cast<int32_t*>(empty + MAX_STAGES);  // a wait ran out; stages issued; shares of the part
+    __shared__ Seg segs[3][MAX_SEGS];
+    const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 1 + 32);  // the weights' announcement, the token warp's lanes
             mbar_init(&empty[i], CONSUMERS / 32);
         }
         flags[0] = flags[1] = 0;
         fence_mbar_init();
-        if (G == 0) {
-            prefetch_tmap(&m2);
-            if (a.hsum) prefetch_tmap(&m2s);
+        if (!S::Q4) {
+            prefetch_tmap(&maps.w13);
+            prefetch_tmap(&maps.w2);
         }
     }
     pdl_trigger();
     pdl_wait();  // the router's logits
     route_batch(a, r);
-    if (tid >= CONSUMERS)
-        produce<G, NT>(a, r, &m2, &m2s, ring, slot, stages, full, empty, &flags[1]);
-    else
-        consume<G, NT>(a, r, ring, slot, stages, full, empty, Hs, red, &flags[0]);
+    if (a.test_stall && blockIdx.x == 0 && warp >= CONSUMERS / 32) {
+        // the test hook: nothing is brought in, the consumers' waits run out
+    } else if (warp == CONSUMERS / 32) {
+        bring_weights<G, NT>(a, r, maps, segs[1], ring, slot, stages, full, empty, &flags[1]);
+    } else if (warp > CONSUMERS / 32) {
+        bring_tokens<G, NT>(a, r, segs[2], ring, slot, stages, full, empty);
+    } else {
+        consume<G, NT>(a, r, segs[0], ring, slot, stages, full, empty, Hs, red, flags);
+    }
     if (blockIdx.x == gridDim.x - 1) publish_routing(a, r);
     __syncthreads();
     if (flags[0] && tid == 0) {
@@ -923,30 +953,30 @@ __global__ void __cluster_dims__(1, RC, 1) __launch_bounds__(256)
 }
 
 template <int G, int NT>
-int launch_ffn(const CUtensorMap& m2, const CUtensorMap& m2s, const FewArgs& a, int smem_limit,
-               cudaStream_t st) {
+int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
     using S = Shape<G, NT>;
     const int slot = S::slot(a.T);
-    int stages = (int)(((size_t)smem_limit - S::fixed()) / slot);
+    // the kernel's few static bytes count too
+    const size_t limit = (size_t)smem_limit - 3 * MAX_SEGS * sizeof(Seg) - 256;
+    int stages = (int)((limit - S::fixed()) / slot);
     stages = stages > MAX_STAGES ? MAX_STAGES : stages;
     const size_t smem = S::fixed() + (size_t)slot * stages;
     auto kern = few_ffn_kernel<G, NT>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_limit) !=
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) !=
         cudaSuccess)
         return launch_result();
-    launch_ex(true, kern, dim3(FEW_CTAS), dim3(FFN_THREADS), smem, st, m2, m2s, a, slot, stages);
+    launch_ex(true, kern, dim3(FEW_CTAS), dim3(FFN_THREADS), smem, st, m, a, slot, stages);
     note_launch();
     return launch_result();
 }
 
 template <int NT>
-int launch_ffn_group(const CUtensorMap& m2, const CUtensorMap& m2s, const FewArgs& a,
-                     int smem_limit, cudaStream_t st) {
+int launch_ffn_group(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
     switch (a.G) {
-        case 0: return launch_ffn<0, NT>(m2, m2s, a, smem_limit, st);
-        case 32: return launch_ffn<32, NT>(m2, m2s, a, smem_limit, st);
-        case 64: return launch_ffn<64, NT>(m2, m2s, a, smem_limit, st);
-        default: return launch_ffn<128, NT>(m2, m2s, a, smem_limit, st);
+        case 0: return launch_ffn<0, NT>(m, a, smem_limit, st);
+        case 32: return launch_ffn<32, NT>(m, a, smem_limit, st);
+        case 64: return launch_ffn<64, NT>(m, a, smem_limit, st);
+        default: return launch_ffn<128, NT>(m, a, smem_limit, st);
     }
 }
 
@@ -977,10 +1007,9 @@ int launch_few_router(const void* x, const float* Wr, float* z, int T, int d, in
     return launch_result();
 }
 
-int launch_few_ffn(const CUtensorMap& m2, const CUtensorMap& m2s, const FewArgs& a, int smem_limit,
-                   cudaStream_t st) {
-    return a.T <= 8 ? launch_ffn_group<1>(m2, m2s, a, smem_limit, st)
-                    : launch_ffn_group<2>(m2, m2s, a, smem_limit, st);
+int launch_few_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
+    return a.T <= 8 ? launch_ffn_group<1>(m, a, smem_limit, st)
+                    : launch_ffn_group<2>(m, a, smem_limit, st);
 }
 
 int launch_few_combine(const FewArgs& a, cudaStream_t st) {

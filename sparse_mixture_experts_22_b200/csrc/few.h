@@ -12,7 +12,7 @@ namespace moe {
 constexpr int FEW_MAX_T = 16;       // tokens of one call
 constexpr int FEW_CTAS = 148;       // CTAs of the expert kernel (one per SM)
 constexpr int FEW_MAX_ITEMS = FEW_MAX_T * 8 + 1;  // experts one batch can hit, and the shared one
-constexpr int FEW_GRAN = 8;         // hidden units per granule, the unit the CTAs share work in
+constexpr int FEW_GRAN = 32;        // hidden units per granule, the unit the CTAs share work in
 constexpr int FEW_HCAP = 512;       // hidden units a part holds in shared memory at most
 
 // ---------------------------------------------------------------- 4-bit layout
@@ -26,18 +26,17 @@ constexpr int FEW_HCAP = 512;       // hidden units a part holds in shared memor
 // registers 0 and 2 are row g, 1 and 3 row g + 8, at k = 2t, 2t + 1 (registers
 // 0, 1) and 2t + 8, 2t + 9 (registers 2, 3).
 //
-// Q13: codes [n][hid/8][d/128][1024 B]: a block is 16 rows (gate rows of hidden
-//      units 8a..8a+7, then their up rows) x 128 of d; inside, [2][32 lanes][4
-//      words], k16 step = 4 * half + word; then the scales
-//      [n][hid/8][d/128][128/G][16 rows] bf16.
+// Q13: blocks [n][hid/32][d/128] of 64 rows x 128 of d: four tiles of 16 rows
+//      (tile i the gate rows of hidden units 8i..8i+7 of the 32, then their up
+//      rows), each [2][32 lanes][4 words] with k16 step = 4 * half + word; then
+//      the scales [128/G][64 rows] bf16.  The columns of one granule follow one
+//      another, so a stage of any depth is one copy.
 // Q2:  codes [n][d/128][hid/32][8 row tiles][32 lanes][2 words]: 128 rows of d x
 //      32 hidden units, tile i its rows 16i..16i+15, word = k16 step; then the
 //      scales [n][d/128][hid/G][128 rows] bf16.
-__host__ __device__ inline size_t q13_code_bytes(int64_t n, int hid, int d) {
-    return (size_t)n * (hid / 8) * (d / 128) * 1024;
-}
+__host__ __device__ constexpr int q13_block_bytes(int G) { return 4096 + 128 * (128 / G); }
 __host__ __device__ inline size_t q13_bytes(int64_t n, int hid, int d, int G) {
-    return (size_t)n * (hid / 8) * (d / 128) * (1024 + (size_t)(128 / G) * 32);
+    return (size_t)n * (hid / 32) * (d / 128) * q13_block_bytes(G);
 }
 __host__ __device__ inline size_t q2_code_bytes(int64_t n, int hid, int d) {
     return (size_t)n * (d / 128) * (hid / 32) * 2048;
@@ -92,10 +91,14 @@ int64_t few_part_rows(int T, int h, int E, int k, int hsum);
 // Logits z [T][E] = x Wr; also clears the status word.
 int launch_few_router(const void* x, const float* Wr, float* z, int T, int d, int E,
                       int32_t* status, cudaStream_t st);
-// m2, m2s: tensor maps of W2p and W2s as rows of the hidden width, boxes of 64
-// columns x 128 rows with the 128-byte swizzle (bf16 weights; else unused).
-int launch_few_ffn(const CUtensorMap& m2, const CUtensorMap& m2s, const FewArgs& a, int smem_limit,
-                   cudaStream_t st);
+// Tensor maps of the bf16 weights (unused with 4 bits): W13 as [blocks of 128
+// rows][128][d] in boxes of 64 columns x 32 rows x 2 blocks (a granule's gate
+// and up rows) with the 128-byte swizzle, W2p as rows of the hidden width in
+// boxes of 32 columns x 128 rows with the 64-byte swizzle; s: the shared set's.
+struct FewMaps {
+    CUtensorMap w13, w2, w13s, w2s;
+};
+int launch_few_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st);
 int launch_few_combine(const FewArgs& a, cudaStream_t st);
 
 }  // namespace moe

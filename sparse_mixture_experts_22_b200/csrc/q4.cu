@@ -4,9 +4,15 @@
 // Per row and group of G weights along the reduction: a = max |w|,
 // s = bf16(a / 7), q = w / s rounded to nearest even and clamped to [-7, 7]
 // (0 where s is 0).  The scale is stored in bf16, half of what fp32 would add
-// to the 4 bits at G = 32; q is taken against the rounded scale, so that the
-// rounding costs nothing but a largest weight that may clip by 2^-9.  Read
-// back, q s is exact in fp32 (4 bits times 8) and rounded once to bf16.
+// to the 4 bits at G = 32; q is taken against the rounded scale, so a largest
+// weight is off by 2^-9 of itself at most.  Read back, q s is exact in fp32 (4
+// bits times 8) and rounded once to bf16.
+//
+// One pass, bound by memory.  A warp takes 16 rows x 128 columns: lane (half,
+// c) reads the eight weights 8c.. of row i (half 0) and row i + 8 (half 1) for i
+// = 0..7, so that a row's 256 bytes are one access and eight are in flight.  The
+// fragment order gathers a word from four lanes (two rows, two runs of eight
+// columns); the lanes exchange their eight codes as one word each.
 #include "common.cuh"
 #include "few.h"
 #include "kernels.h"
@@ -15,201 +21,175 @@ namespace moe {
 
 namespace {
 
-// Row of the packed matrix that row r of a 16-row block holds: gate rows of
-// hidden units 8a.. (r < 8), their up rows, or plainly row base + r.
-__device__ __forceinline__ int64_t w13_row(int64_t e, int hid, int a, int r) {
-    const int j = a * 8 + r % 8;
-    return e * 2 * hid + 256 * (j / 128) + 128 * (r / 8) + j % 128;
-}
-
-__device__ __forceinline__ float quad_max(float v) {
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-
-__device__ __forceinline__ uint32_t code_of(float w, float s) {
-    const float q = s > 0.f ? rintf(w / s) : 0.f;
-    return (uint32_t)((int)fminf(fmaxf(q, -7.f), 7.f) + 8);
-}
-
-// A lane's fragment of 16 rows x 16 STEPS columns: v[s][2 reg + element].
-// lo / hi: rows g and g + 8 of the block at its first column.
-template <int STEPS>
-__device__ __forceinline__ void load_frag(const __nv_bfloat16* lo, const __nv_bfloat16* hi,
-                                          float (*v)[8]) {
-    const int t = threadIdx.x & 3;
+// max |w| over the lanes of a group (G / 8 neighbours)
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)
+    for (int o = 1; o < G / 8; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// Codes of eight weights, nibble e = q + 8 of element e.  q = rint(w / s) without
+// eight divisions: w inv is within 2^-20 of the quotient, and as w and s have 8
+// significant bits and |w / s| <= 7.03, the quotient is either n + 1/2 exactly or
+// at least 2^-10 away from it; the exact remainder tells the half and sends it
+// to the even code.
+__device__ __forceinline__ uint32_t codes_of(const float* w, float s) {
+    uint32_t out = 0;
+    if (s >= 1.1754944e-38f) {
+        const float inv = 1.f / s, half = 0.5f * s;
 #pragma unroll
-        for (int reg = 0; reg < 4; ++reg) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                (reg & 1 ? hi : lo) + 16 * s + 8 * (reg >> 1) + 2 * t);
-            v[s][2 * reg] = __uint_as_float(w << 16);
-            v[s][2 * reg + 1] = __uint_as_float(w & 0xFFFF0000u);
+        for (int e = 0; e < 8; ++e) {
+            float q = rintf(w[e] * inv);
+            const float rest = fmaf(-q, s, w[e]);
+            int code = (int)q;
+            if (fabsf(rest) == half && (code & 1)) code += rest > 0.f ? 1 : -1;
+            out |= (uint32_t)(min(max(code, -7), 7) + 8) << (4 * e);
         }
-}
-
-template <int STEPS>
-__device__ __forceinline__ void store_frag(__nv_bfloat16* lo, __nv_bfloat16* hi, float (*v)[8]) {
-    const int t = threadIdx.x & 3;
+    } else {  // no scale, or one below the normal range
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-        for (int reg = 0; reg < 4; ++reg)
-            *reinterpret_cast<uint32_t*>((reg & 1 ? hi : lo) + 16 * s + 8 * (reg >> 1) + 2 * t) =
-                pack_bf16x2(v[s][2 * reg], v[s][2 * reg + 1]);
+        for (int e = 0; e < 8; ++e) {
+            const float q = s > 0.f ? rintf(w[e] / s) : 0.f;
+            out |= (uint32_t)((int)fminf(fmaxf(q, -7.f), 7.f) + 8) << (4 * e);
+        }
+    }
+    return out;
 }
 
-// max |w| of a lane's elements of row g (half 0) or g + 8 in step s
-__device__ __forceinline__ float step_max(const float* v, int half) {
-    return fmaxf(fmaxf(fabsf(v[2 * half]), fabsf(v[2 * half + 1])),
-                 fmaxf(fabsf(v[2 * half + 4]), fabsf(v[2 * half + 5])));
-}
-
-// Codes of one step; sl, sh: the scales of rows g and g + 8.
-__device__ __forceinline__ uint32_t pack_step(const float* v, float sl, float sh) {
+// The lanes' codes (lane (half, c): row g + 8 half, columns 8c..) as fragment
+// words: lane (t, s) = 8t + s gets the word of fragment lane 4g + t, k16 step s.
+__device__ __forceinline__ uint32_t to_fragment(uint32_t codes) {
+    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7;
     uint32_t w = 0;
 #pragma unroll
     for (int reg = 0; reg < 4; ++reg) {
-        const float s = reg & 1 ? sh : sl;
-        w |= code_of(v[2 * reg], s) << (4 * reg);
-        w |= code_of(v[2 * reg + 1], s) << (4 * reg + 16);
+        const uint32_t c = __shfl_sync(0xffffffffu, codes, (reg & 1) * 16 + 2 * s + (reg >> 1));
+        const uint32_t two = c >> (8 * t);
+        w |= (two & 15u) << (4 * reg) | (two >> 4 & 15u) << (4 * reg + 16);
     }
     return w;
 }
 
-__device__ __forceinline__ void unpack_step(uint32_t w, float sl, float sh, float* v) {
+// The other way: fragment words of lanes (t, s) to the eight codes of lane (half, c).
+__device__ __forceinline__ uint32_t from_fragment(uint32_t w) {
+    const int lane = threadIdx.x & 31, reg = 2 * (lane & 1) + (lane >> 4), s = (lane & 15) >> 1;
+    uint32_t codes = 0;
 #pragma unroll
-    for (int reg = 0; reg < 4; ++reg) {
-        const float s = reg & 1 ? sh : sl;
-        v[2 * reg] = (float)((int)((w >> (4 * reg)) & 15u) - 8) * s;
-        v[2 * reg + 1] = (float)((int)((w >> (4 * reg + 16)) & 15u) - 8) * s;
+    for (int t = 0; t < 4; ++t) {
+        const uint32_t two = __shfl_sync(0xffffffffu, w, 8 * t + s) >> (4 * reg);
+        codes |= (two & 15u) << (8 * t) | (two >> 16 & 15u) << (8 * t + 4);
+    }
+    return codes;
+}
+
+// 16 rows x 128 columns of bf16 weights at W (ld elements a row; row i and row
+// i + 8 begin at W + i ld and W + up + i ld) <-> codes and scales.  word(g):
+// where lane (t, s) keeps the word of fragment lane 4g + t; scale(q, r): the
+// scale of group q, row r.
+template <int G, bool QUANT, typename Word, typename Scale>
+__device__ __forceinline__ void block_pass(__nv_bfloat16* W, int64_t ld, int64_t up, Word word,
+                                           Scale scale) {
+    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
+    __nv_bfloat16* row = W + (half ? up : 0) + c * 8;
+    if (QUANT) {
+        uint4 raw[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) raw[g] = __ldcs(reinterpret_cast<const uint4*>(row + g * ld));
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            const uint32_t u[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+            float w[8], m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                w[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16);
+                m = fmaxf(m, fabsf(w[e]));
+            }
+            const float s = bf16_round(group_max<G>(m) / 7.f);
+            if (c % (G / 8) == 0) *scale(c / (G / 8), g + 8 * half) = __float2bfloat16_rn(s);
+            *word(g) = to_fragment(codes_of(w, s));
+        }
+    } else {
+        uint32_t words[8];
+        float s[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            words[g] = *word(g);
+            s[g] = __bfloat162float(*scale(c / (G / 8), g + 8 * half));
+        }
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            const uint32_t codes = from_fragment(words[g]);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = (float)((int)(codes >> (4 * e) & 15u) - 8) * s[g];
+            uint4 o;
+            o.x = pack_bf16x2(v[0], v[1]);
+            o.y = pack_bf16x2(v[2], v[3]);
+            o.z = pack_bf16x2(v[4], v[5]);
+            o.w = pack_bf16x2(v[6], v[7]);
+            *reinterpret_cast<uint4*>(row + g * ld) = o;
+        }
     }
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return bf16_round(amax / 7.f); }
-
-// One warp per 16 x 128 block of W13.
+// One warp per tile of 16 rows x 128 columns of W13.
 template <int G, bool QUANT>
 __global__ void __launch_bounds__(256)
-    q13_kernel(__nv_bfloat16* W13, uint32_t* codes, __nv_bfloat16* scales, int64_t blocks, int hid,
-               int d) {
-    constexpr int SG = G / 16;
-    const int lane = threadIdx.x & 31, g = lane >> 2;
+    q13_kernel(__nv_bfloat16* W13, uint8_t* Q13, int64_t tiles, int hid, int d) {
+    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t b = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); b < blocks;
-         b += warps) {
+    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < tiles;
+         i += warps) {
+        const int64_t b = i >> 2;   // block of 32 hidden units x 128 columns
+        const int tile = (int)(i & 3);
         const int kb = (int)(b % (d / 128));
-        const int64_t ea = b / (d / 128);
-        const int a = (int)(ea % (hid / 8));
-        const int64_t e = ea / (hid / 8);
-        __nv_bfloat16* lo = W13 + w13_row(e, hid, a, g) * d + kb * 128;
-        __nv_bfloat16* hi = W13 + w13_row(e, hid, a, g + 8) * d + kb * 128;
-        uint32_t* cw = codes + b * 256 + lane * 4;
-        __nv_bfloat16* sc = scales + b * (128 / G) * 16;
-        float v[8][8];
-        if (QUANT) {
-            load_frag<8>(lo, hi, v);
-#pragma unroll
-            for (int q = 0; q < 128 / G; ++q) {
-                float ml = 0.f, mh = 0.f;
-#pragma unroll
-                for (int s = 0; s < SG; ++s) {
-                    ml = fmaxf(ml, step_max(v[q * SG + s], 0));
-                    mh = fmaxf(mh, step_max(v[q * SG + s], 1));
-                }
-                const float sl = scale_of(quad_max(ml)), sh = scale_of(quad_max(mh));
-                if ((lane & 3) == 0) {
-                    sc[q * 16 + g] = __float2bfloat16_rn(sl);
-                    sc[q * 16 + 8 + g] = __float2bfloat16_rn(sh);
-                }
-#pragma unroll
-                for (int s = 0; s < SG; ++s) {
-                    const int st = q * SG + s;
-                    cw[(st / 4) * 128 + st % 4] = pack_step(v[st], sl, sh);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int st = 0; st < 8; ++st) {
-                const int q = st / SG;
-                unpack_step(cw[(st / 4) * 128 + st % 4], __bfloat162float(sc[q * 16 + g]),
-                            __bfloat162float(sc[q * 16 + 8 + g]), v[st]);
-            }
-            store_frag<8>(lo, hi, v);
-        }
+        const int64_t unit = b / (d / 128) * 32 + tile * 8;  // over all experts: e * hid + j
+        const int64_t gate = 256 * (unit / 128) + unit % 128;
+        uint8_t* blk = Q13 + b * q13_block_bytes(G);
+        uint32_t* codes = reinterpret_cast<uint32_t*>(blk) + tile * 256 + (s >> 2) * 128 + (s & 3);
+        __nv_bfloat16* sc = reinterpret_cast<__nv_bfloat16*>(blk + 4096) + tile * 16;
+        block_pass<G, QUANT>(
+            W13 + gate * d + kb * 128, d, (int64_t)128 * d,
+            [&](int g) { return codes + (4 * g + t) * 4; },
+            [&](int q, int r) { return sc + q * 64 + r; });
     }
 }
 
 // One warp per 16 rows x 128 hidden units of W2p.
 template <int G, bool QUANT>
 __global__ void __launch_bounds__(256)
-    q2_kernel(__nv_bfloat16* W2p, uint32_t* codes, __nv_bfloat16* scales, int64_t blocks, int hid,
-              int d) {
-    constexpr int SG = G / 16;
-    const int lane = threadIdx.x & 31, g = lane >> 2;
+    q2_kernel(__nv_bfloat16* W2p, uint32_t* Q2, __nv_bfloat16* scales, int64_t tiles, int hid) {
+    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7;
     const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t b = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); b < blocks;
-         b += warps) {
-        const int kb = (int)(b % (hid / 128));         // 128 hidden units
-        const int64_t tile = b / (hid / 128);          // 16 rows of all experts' d
-        const int64_t rb = tile / 8;
-        const int ti = (int)(tile % 8);
-        __nv_bfloat16* lo = W2p + (tile * 16 + g) * hid + kb * 128;
-        __nv_bfloat16* hi = lo + (int64_t)8 * hid;
-        uint32_t* cw = codes + ((rb * (hid / 32) + kb * 4) * 8 + ti) * 64 + lane * 2;
-        __nv_bfloat16* sc = scales + (rb * (hid / G) + kb * (128 / G)) * 128 + ti * 16;
-        float v[8][8];
-        if (QUANT) {
-            load_frag<8>(lo, hi, v);
-#pragma unroll
-            for (int q = 0; q < 128 / G; ++q) {
-                float ml = 0.f, mh = 0.f;
-#pragma unroll
-                for (int s = 0; s < SG; ++s) {
-                    ml = fmaxf(ml, step_max(v[q * SG + s], 0));
-                    mh = fmaxf(mh, step_max(v[q * SG + s], 1));
-                }
-                const float sl = scale_of(quad_max(ml)), sh = scale_of(quad_max(mh));
-                if ((lane & 3) == 0) {
-                    sc[q * 128 + g] = __float2bfloat16_rn(sl);
-                    sc[q * 128 + 8 + g] = __float2bfloat16_rn(sh);
-                }
-#pragma unroll
-                for (int s = 0; s < SG; ++s) {
-                    const int st = q * SG + s;
-                    cw[(st / 2) * 512 + st % 2] = pack_step(v[st], sl, sh);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int st = 0; st < 8; ++st) {
-                const int q = st / SG;
-                unpack_step(cw[(st / 2) * 512 + st % 2], __bfloat162float(sc[q * 128 + g]),
-                            __bfloat162float(sc[q * 128 + 8 + g]), v[st]);
-            }
-            store_frag<8>(lo, hi, v);
-        }
+    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < tiles;
+         i += warps) {
+        const int kb = (int)(i % (hid / 128));
+        const int64_t row = i / (hid / 128) * 16, rb = row / 128;  // over all experts' d rows
+        const int tile = (int)(row % 128) / 16;
+        uint32_t* codes = Q2 + ((rb * (hid / 32) + kb * 4 + (s >> 1)) * 8 + tile) * 64 + (s & 1);
+        __nv_bfloat16* sc = scales + (rb * (hid / G) + kb * (128 / G)) * 128 + tile * 16;
+        block_pass<G, QUANT>(
+            W2p + row * hid + kb * 128, hid, (int64_t)8 * hid,
+            [&](int g) { return codes + (4 * g + t) * 2; },
+            [&](int q, int r) { return sc + q * 128 + r; });
     }
 }
 
 template <int G, bool QUANT>
 int launch_q4(const void* W13, const void* W2p, const void* Q13, const void* Q2, int n, int hid,
               int d, cudaStream_t st) {
-    const int64_t blocks = (int64_t)n * (hid / 8) * (d / 128);
-    const int grid = (int)((blocks + 7) / 8 < 16384 ? (blocks + 7) / 8 : 16384);
-    uint8_t* q13 = reinterpret_cast<uint8_t*>(const_cast<void*>(Q13));
+    auto grid = [](int64_t tiles) { return (int)((tiles + 7) / 8 < 1184 ? (tiles + 7) / 8 : 1184); };
     uint8_t* q2 = reinterpret_cast<uint8_t*>(const_cast<void*>(Q2));
-    q13_kernel<G, QUANT><<<grid, 256, 0, st>>>(
-        reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(W13)), reinterpret_cast<uint32_t*>(q13),
-        reinterpret_cast<__nv_bfloat16*>(q13 + q13_code_bytes(n, hid, d)), blocks, hid, d);
+    const int64_t t13 = (int64_t)n * (hid / 8) * (d / 128);
+    q13_kernel<G, QUANT><<<grid(t13), 256, 0, st>>>(
+        reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(W13)),
+        reinterpret_cast<uint8_t*>(const_cast<void*>(Q13)), t13, hid, d);
     note_launch();
     if (launch_result() != 0) return -1;
-    const int64_t blocks2 = (int64_t)n * (d / 16) * (hid / 128);
-    const int grid2 = (int)((blocks2 + 7) / 8 < 16384 ? (blocks2 + 7) / 8 : 16384);
-    q2_kernel<G, QUANT><<<grid2, 256, 0, st>>>(
+    const int64_t t2 = (int64_t)n * (d / 16) * (hid / 128);
+    q2_kernel<G, QUANT><<<grid(t2), 256, 0, st>>>(
         reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(W2p)), reinterpret_cast<uint32_t*>(q2),
-        reinterpret_cast<__nv_bfloat16*>(q2 + q2_code_bytes(n, hid, d)), blocks2, hid, d);
+        reinterpret_cast<__nv_bfloat16*>(q2 + q2_code_bytes(n, hid, d)), t2, hid);
     note_launch();
     return launch_result();
 }

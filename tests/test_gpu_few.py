@@ -255,12 +255,13 @@ def test_unread_experts_may_hold_nan(group):
     for e in range(wl.E):
         if e not in hit:
             for w in layer._held[2:4]:
-                if group:
-                    # codes of every expert come first, then the scales of every expert
-                    codes = {True: wl.h // 8 * (wl.d // 128) * 1024,
-                             False: wl.d // 128 * (wl.h // 32) * 2048}[w is layer._held[2]]
-                    scales = w[wl.E * codes:].view(torch.bfloat16).view(wl.E, -1)
-                    scales[e] = float("nan")
+                if group and w is layer._held[2]:
+                    # blocks of codes and their scales: all bits set make the scales NaN
+                    w.view(wl.E, -1)[e] = 255
+                elif group:
+                    # the codes of every expert come first, then the scales of every expert
+                    codes = wl.E * (wl.d // 128) * (wl.h // 32) * 2048
+                    w[codes:].view(wl.E, -1)[e] = 255
                 else:
                     w[e] = float("nan")
     F.check(run(layer, g["x"]), ref)
