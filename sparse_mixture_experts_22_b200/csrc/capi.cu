@@ -1750,8 +1750,8 @@ static_assert(MOE_FEW_MAX_T == FEW_MAX_T, "token limits differ");
 // Workspace of the few-token layer.
 struct FewPlan {
     Plan P;
-    size_t off_logits, off_table, off_ppart, off_hpart, off_cnt, off_idx, off_gate, off_sums,
-        off_part, total;
+    size_t off_logits, off_table, off_xq, off_xf, off_ppart, off_hpart, off_cnt, off_idx, off_gate,
+        off_sums, off_part, total;
 };
 
 static int few_plan_or_fail(const moe_config* cfg, FewPlan* f) {
@@ -1769,6 +1769,8 @@ static int few_plan_or_fail(const moe_config* cfg, FewPlan* f) {
     const size_t T = (size_t)P.T, E = (size_t)P.E, k = (size_t)P.k;
     f->off_logits = take(T * E * 4);
     f->off_table = take(T * (k + 1) * sizeof(int4));
+    f->off_xq = take(T * 3 * (size_t)P.d);
+    f->off_xf = take(T * 4);
     f->off_ppart = take(E * 4);
     f->off_hpart = take(4);
     f->off_cnt = take(E * 4);
@@ -1840,6 +1842,8 @@ static int few_forward(const moe_config* cfg, int32_t group, const void* x, cons
     FewArgs a;
     memset(&a, 0, sizeof a);
     a.x = x;
+    a.xq = at<int8_t>(ws, F.off_xq);
+    a.xf = at<float>(ws, F.off_xf);
     a.logits = at<float>(ws, F.off_logits);
     a.bias = cfg->has_bias ? bias : nullptr;
     a.w13 = w13;
@@ -1871,9 +1875,7 @@ static int few_forward(const moe_config* cfg, int32_t group, const void* x, cons
         if (P.S > 0) MOE_TRY(few_maps(&maps.w13s, &maps.w2s, w13s, w2s, 1, P.hsum, P.d));
     }
     trace_pre(st, "few_router");
-    MOE_TRY(launched(launch_few_router(x, Wr, at<float>(ws, F.off_logits), a.T, P.d, P.E, a.status,
-                                       st),
-                     "few_router"));
+    MOE_TRY(launched(launch_few_router(a, Wr, at<float>(ws, F.off_logits), st), "few_router"));
     trace_mark(st, "few_router");
     trace_pre(st, "few_ffn");
     MOE_TRY(launched(launch_few_ffn(maps, a, dv.smem_optin, st), "few_ffn"));

@@ -268,16 +268,27 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The eight codes of a word as an A fragment: or-ing a nibble u = q + 8 into the
-// mantissa of 128 gives the bf16 128 + u, and 128 + u - 136 = q is exact.
-__device__ __forceinline__ void codes_to_frag(uint32_t w, uint32_t (&a)[4]) {
-    const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), off);
-        a[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+// c (16 x 8, int32) += a (16 x 32) b (32 x 8), signed 8-bit
+__device__ __forceinline__ void imma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                     uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// c += 16 q by b for the 32 columns of two code words.
+__device__ __forceinline__ void imma_codes(int (&c)[4], uint32_t w0, uint32_t w1, uint32_t b0,
+                                           uint32_t b1) {
+    constexpr uint32_t M = 0xF0F0F0F0u;
+    imma(c, w0 & M, (w0 << 4) & M, w1 & M, (w1 << 4) & M, b0, b1);
+}
+
+// An integer of magnitude below 2^22 to fp32 (an addition instead of the slower
+// conversion): a group's sum is at most 128 * 112 * 128 = 1.84 million.
+__device__ __forceinline__ float small_int(int v) {
+    return __int_as_float(v + 0x4B400000) - 12582912.f;
 }
 
 __device__ __forceinline__ float lds_bf16(uint32_t addr) {
@@ -289,48 +300,69 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 // ---------------------------------------------------------------- the expert kernel
 //
 // Sixteen warps multiply what two others bring in through a ring of stages:
-// one issues the weights' copies (tensor maps for bf16, one bulk copy per stage
-// for 4 bits), the other copies the expert's token rows 16 bytes a lane; both
-// signal the stage's mbarrier.  Weights are the A operand (16 rows), the tokens
-// of one expert the B operand (8 columns a tile), so one instruction takes 256
+// one issues the weights' copies (tensor maps for bf16, bulk copies for 4 bits),
+// the other copies the expert's token rows 16 bytes a lane; both signal the
+// stage's mbarrier.  Weights are the A operand (16 rows), the tokens of one
+// expert the B operand (8 columns a tile), so one instruction takes 256 or 512
 // weights from registers whatever the number of tokens.
 //
 // First half, per granule (32 hidden units): four tiles of 16 rows, the gate and
 // the up rows of 8 units each, so that a lane's accumulators hold both for the
-// same unit and token.  KW warps share the columns of a stage; their sums meet
-// in shared memory at the end of d, where H = g silu(a) u is formed in fp32 and
-// stored as two bf16 parts.  Second half: 256 rows of w2 (16 a warp) by the
-// part's columns against both parts of H; the products of one expert go to the
-// part's own rows of the partial outputs.
+// same unit and token.  Four warps share a tile's columns; their sums meet in
+// shared memory at the end of d, where H = g silu(a) u is formed in fp32.  The
+// four groups of warps wait for nothing of one another.  Second half: 256 rows of
+// w2 (16 a warp) by the part's columns against H; the products of one expert go
+// to the part's own rows of the partial outputs.
 //
-// Copied bf16 tiles are swizzled and token rows pitched by 16 bytes, so that
-// ldmatrix meets no bank twice; 4-bit codes arrive in fragment order and are
-// read as they lie.
-template <int G, int NT>
+// bf16 weights: m16n8k16 products with fp32 sums, H as two bf16 parts.
+//
+// 4-bit weights: the products are exact.  A row of x is an integer of 23 bits
+// times a power of two (of the row's largest magnitude: the rounding is 2^-22 of
+// that at most, what an fp32 sum of the row loses too), held as three planes of
+// signed 8-bit digits; H likewise per expert and part.  The planes are columns of
+// one 8-bit product, which takes the codes after two masks and a shift per 8
+// codes -- as bf16 fragments they took three shifts, four masks and four
+// subtractions, and 30 clocks per 256 weights and scheduler against 11, where HBM
+// brings 256 in 23.  Sums within a group are exact in int32; a group's scale
+// multiplies its sum in fp32.  Two tokens' planes fit one tile of 8 columns
+// ("packed"); more take a tile per plane and 8 tokens.
+//
+// Copied bf16 tiles are swizzled and token rows pitched by an odd multiple of 16
+// bytes, so that ldmatrix meets no bank twice; codes arrive in fragment order and
+// are read as they lie.
+template <int G, int TT>   // group (0: bf16), most tokens
 struct Shape {
     static constexpr bool Q4 = G > 0;
     static constexpr int GG = Q4 ? G : 128;
+    static constexpr int NT = (TT + 7) / 8;                // tiles of 8 tokens
     static constexpr int KP = Q4 ? 128 : 64;               // columns of a warp in a stage
-    static constexpr int KW = Q4 && NT == 1 ? 8 : 4;       // warps along the columns
+    static constexpr int KW = 4;                           // warps along the columns
     static constexpr int KA = KW * KP;                     // columns of a stage
-    static constexpr int GW = 16 / KW;                     // warps along the 16-row tiles
-    static constexpr int MW = 4 / GW;                      // tiles of a warp
     static constexpr int QB = q13_block_bytes(GG);
-    static constexpr int XPITCH = KA * 2 + 16;             // bytes of a token's row in a stage
-    static constexpr int XOFF = Q4 ? KA / 128 * QB : KA * 128;  // where its tokens begin
-    // down: 2 blocks of 128 rows x 8 panels of 32 units (4 bits) or 2 (bf16)
-    static constexpr int PANELS = Q4 ? 8 : 2;
-    static constexpr int SCALES = 32768;                   // 4 bits: where its scales begin
-    static constexpr int GROUPS = GG == 32 ? 8 : 256 / GG + 1;  // groups that 8 panels can meet
-    static constexpr int HPITCH = (FEW_HCAP + 8) * 2;      // bytes of a token's row of H
+    static constexpr int XROWS = Q4 ? 3 : 1;               // rows of a stage per token
+    static constexpr int XBYTES = Q4 ? 1 : 2;              // bytes of an element
+    static constexpr int XPITCH = KA * XBYTES + 16;
+    static constexpr int XOFF = Q4 ? KA / 128 * QB : KA * 128;  // where the tokens begin
+    // second half: 2 blocks of 128 rows x panels of 32 units
+    static constexpr int PANELS = Q4 ? (TT <= 2 ? 4 : 8) : 2;
+    static constexpr int ROWBLK = Q4 ? PANELS * 2048 : 8192;    // bytes of a block of rows
+    static constexpr int SCALES = 2 * PANELS * 2048;            // 4 bits: where its scales begin
+    // groups that the panels can meet
+    static constexpr int GROUPS = GG == 32 ? PANELS : PANELS * 32 / GG + 1;
+    // H: bf16 high then low parts [2][NT * 8][HPITCH]; 4 bits [TT][HPITCH], a row
+    // first fp32, then its three planes HPLANE bytes apart
+    static constexpr int HPLANE = FEW_HCAP + 32;
+    static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 16 : (FEW_HCAP + 8) * 2;
     static constexpr int HPART = NT * 8 * HPITCH;
-    static constexpr int RED = 16 * MW * NT * 8 * 20 * 4;  // bytes of the warps' sums
+    static constexpr int HBYTES = Q4 ? TT * HPITCH : 2 * HPART;
+    static constexpr int RED = 2 * 16 * NT * 640;          // the warps' sums, two granules
     static __host__ __device__ int slot(int T) {
-        const int up = XOFF + T * XPITCH, down = Q4 ? SCALES + 2 * GROUPS * 256 : 32768;
+        const int up = XOFF + T * XROWS * XPITCH;
+        const int down = Q4 ? SCALES + 2 * GROUPS * 256 : 32768;
         return ((up > down ? up : down) + 1023) / 1024 * 1024;
     }
     static __host__ __device__ size_t fixed() {
-        return 1024 + 2 * HPART + RED + sizeof(Routing) + 512;
+        return 1024 + (HBYTES + 15) / 16 * 16 + RED + sizeof(Routing) + 512;
     }
 };
 
@@ -394,10 +426,10 @@ struct Ring {
 // down(seg, r0, p0, np) for every stage of the second (r0 the first of up to 256
 // rows of d, np panels of 32 units from panel p0 of the share) of all parts of
 // this block, in ring order; a call that returns false ends it.
-template <int G, int NT, typename Up, typename Down>
+template <int G, int TT, typename Up, typename Down>
 __device__ __forceinline__ void for_stages(const FewArgs& a, const Routing& r, Seg* segs, Up up,
                                            Down down) {
-    using S = Shape<G, NT>;
+    using S = Shape<G, TT>;
     for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
         const int n = segments(a, r, v, segs);
         for (int i = 0; i < n; ++i)
@@ -412,11 +444,11 @@ __device__ __forceinline__ void for_stages(const FewArgs& a, const Routing& r, S
 }
 
 // The weights' copies.
-template <int G, int NT>
+template <int G, int TT>
 __device__ void bring_weights(const FewArgs& a, const Routing& r, const FewMaps& maps, Seg* segs,
                               uint8_t* ring, int slot, int stages, uint64_t* full,
                               uint64_t* empty, int32_t* issued) {
-    using S = Shape<G, NT>;
+    using S = Shape<G, TT>;
     const int lane = threadIdx.x & 31;
     const int d = a.d;
     const uint64_t once = l2_policy_evict_first();
@@ -469,7 +501,7 @@ __device__ void bring_weights(const FewArgs& a, const Routing& r, const FewMaps&
             const int b = lane & 1;
             const int64_t rb = (int64_t)e * (d / 128) + r0 / 128 + b;
             if (b < nb && lane < 2)
-                bulk_load(smem_addr(dst) + b * 16384, W + (rb * (hid / 32) + pp) * 2048, np * 2048,
+                bulk_load(smem_addr(dst) + b * S::ROWBLK, W + (rb * (hid / 32) + pp) * 2048, np * 2048,
                           &full[p.stage], once);
             if (b < nb && (lane >> 1) == 1)
                 bulk_load(smem_addr(dst) + S::SCALES + b * S::GROUPS * 256,
@@ -484,17 +516,17 @@ __device__ void bring_weights(const FewArgs& a, const Routing& r, const FewMaps&
         p.next();
         return true;
     };
-    for_stages<G, NT>(a, r, segs, up, down);
+    for_stages<G, TT>(a, r, segs, up, down);
 }
 
-// The token rows of the first half, 16 bytes a lane; every lane arrives on
-// every stage, when its copies have landed.
-template <int G, int NT>
+// The token rows of the first half (x, or its planes), 16 bytes a lane; every
+// lane arrives on every stage, when its copies have landed.
+template <int G, int TT>
 __device__ void bring_tokens(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring,
                              int slot, int stages, uint64_t* full, uint64_t* empty) {
-    using S = Shape<G, NT>;
+    using S = Shape<G, TT>;
     const int lane = threadIdx.x & 31;
-    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(a.x);
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(S::Q4 ? (const void*)a.xq : a.x);
     Ring p;
     p.stages = stages;
     auto open = [&]() -> bool {
@@ -503,15 +535,17 @@ __device__ void bring_tokens(const FewArgs& a, const Routing& r, Seg* segs, uint
     };
     auto up = [&](const Seg& s, int, int k0) -> bool {
         if (!open()) return false;
-        const int vecs = min(S::KA, a.d - k0) / 8;
-        const uint32_t dst = smem_addr(ring + (size_t)p.stage * slot) + S::XOFF;
-        for (int n = 0; n < s.n; ++n) {
-            const __nv_bfloat16* src = x + (int64_t)r.tok[s.item][n] * a.d + k0;
+        static_assert(S::KA * S::XBYTES == 512, "one 16-byte copy of every lane is a row");
+        const bool mine = lane * 16 < (a.d - k0) * S::XBYTES;
+        const uint32_t dst = smem_addr(ring + (size_t)p.stage * slot) + S::XOFF + lane * 16;
+        if (mine)
+            for (int n = 0; n < s.n; ++n) {
+                const int64_t row = (int64_t)r.tok[s.item][n] * S::XROWS;
 #pragma unroll
-            for (int q = 0; q < S::KA / 256; ++q)
-                if (q * 32 + lane < vecs)
-                    cp_async16(dst + n * S::XPITCH + (q * 32 + lane) * 16, src + (q * 32 + lane) * 8);
-        }
+                for (int q = 0; q < S::XROWS; ++q)
+                    cp_async16(dst + (n * S::XROWS + q) * S::XPITCH,
+                               x + ((row + q) * a.d + k0) * S::XBYTES + lane * 16);
+            }
         cp_async_arrive(&full[p.stage]);
         p.next();
         return true;
@@ -522,38 +556,378 @@ __device__ void bring_tokens(const FewArgs& a, const Routing& r, Seg* segs, uint
         p.next();
         return true;
     };
-    for_stages<G, NT>(a, r, segs, up, down);
+    for_stages<G, TT>(a, r, segs, up, down);
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-template <int G, int NT>
-__device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring, int slot,
-                        int stages, uint64_t* full, uint64_t* empty, uint8_t* Hs, float* red,
-                        int32_t* flags) {
-    using S = Shape<G, NT>;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int kw = warp % S::KW, gw = warp / S::KW;
-    const int fg = lane >> 2, ft = lane & 3;         // row and column pair of a fragment
-    const int lm = lane & 7, lq = lane >> 3;         // row and matrix of an ldmatrix address
-    const int d = a.d;
-    const uint32_t hs = smem_addr(Hs);
+// What a multiplying warp knows of its place and of the ring.
+struct Consumer {
+    uint8_t* ring;
+    uint64_t *full, *empty;
+    int32_t* flags;
+    int32_t* status;
+    uint64_t limit;
+    int slot;
     Ring p;
-    p.stages = stages;
     bool lost = false;  // a wait ran out: go on without waiting, so that the barriers are met
-    auto wait = [&]() -> uint32_t {
-        if (!lost && !mbar_wait(&full[p.stage], p.phase, a.wait_limit_ns)) {
+
+    __device__ __forceinline__ uint8_t* wait() {
+        if (!lost && !mbar_wait(&full[p.stage], p.phase, limit)) {
             lost = true;
             flags[0] = 1;
-            report_timeout(a.status);
+            report_timeout(status);
         }
         lost = __any_sync(0xffffffffu, lost);
-        return smem_addr(ring + (size_t)p.stage * slot);
-    };
-    auto done = [&]() {
+        return ring + (size_t)p.stage * slot;
+    }
+    __device__ __forceinline__ void done() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[p.stage]);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[p.stage]);
         p.next();
-    };
+    }
+};
+
+// Sum of a quad's lanes.
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// First half, bf16: this warp's sums over d of tile gw's rows by the expert's
+// tokens.  red: where they go, [NT][8 tokens][20] floats.
+template <int TT>
+__device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float* red) {
+    using S = Shape<0, TT>;
+    constexpr int NT = S::NT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
+    const int lm = lane & 7, lq = lane >> 3;         // row and matrix of an ldmatrix address
+    // rows of tokens past the expert's repeat its last one: their columns of the
+    // product are never read
+    uint32_t xrow[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        xrow[nt] = S::XOFF + min(nt * 8 + lm, s.n - 1) * S::XPITCH + (kw * S::KP + lq * 8) * 2;
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[nt][q] = 0.f;
+    for (int k0 = 0; k0 < d; k0 += S::KA) {
+        const uint32_t st = smem_addr(c.wait());
+        if (!c.lost && k0 + kw * S::KP < d) {
+            uint32_t b[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                if (nt * 8 < s.n) {
+                    ldmatrix4(st + xrow[nt], b[nt][0]);
+                    ldmatrix4(st + xrow[nt] + 64, b[nt][1]);
+                }
+            // box of this warp's 64 columns: 32 gate rows, 32 up rows
+            const uint32_t wa = st + kw * 8192 + ((lq & 1) * 32 + gw * 8 + lm) * 128;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t f[4];
+                ldmatrix4(wa + (((u * 2 + (lq >> 1)) ^ lm) << 4), f);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    if (nt * 8 < s.n)
+                        mma(acc[nt], f, b[nt][u / 2][2 * (u & 1)], b[nt][u / 2][2 * (u & 1) + 1]);
+            }
+        }
+        c.done();
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float* q = red + nt * 160 + 2 * (lane & 3) * 20 + (lane >> 2);
+        q[0] = acc[nt][0];
+        q[20] = acc[nt][1];
+        q[8] = acc[nt][2];
+        q[28] = acc[nt][3];
+    }
+}
+
+// The same for 4 bits; packed: the columns are (token, plane), else one tile per
+// plane, joined before they are written.
+template <int G, int TT, bool PACKED>
+__device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* red) {
+    using S = Shape<G, TT>;
+    constexpr int NT = PACKED ? 1 : S::NT, PL = PACKED ? 1 : 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
+    const int lm = lane & 7, lq = lane >> 3;
+    uint32_t xrow[NT][PL];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl) {
+            const int row = PACKED ? min(lm, 3 * s.n - 1) : 3 * min(nt * 8 + lm, s.n - 1) + pl;
+            xrow[nt][pl] = S::XOFF + row * S::XPITCH + kw * S::KP + lq * 16;
+        }
+    float acc[NT][PL][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[nt][pl][q] = 0.f;
+    for (int k0 = 0; k0 < d; k0 += S::KA) {
+        const uint8_t* stp = c.wait();
+        const uint32_t st = smem_addr(stp);
+        if (!c.lost && k0 + kw * S::KP < d) {
+            const uint4* cw = reinterpret_cast<const uint4*>(stp + kw * S::QB + gw * 1024);
+            uint32_t w[8];
+            *reinterpret_cast<uint4*>(w) = cw[lane];
+            *reinterpret_cast<uint4*>(w + 4) = cw[32 + lane];
+            const uint32_t sa = st + kw * S::QB + 4096 + (gw * 16 + (lane >> 2)) * 2;
+            float sl[128 / S::GG], sh[128 / S::GG];
+#pragma unroll
+            for (int q = 0; q < 128 / S::GG; ++q) {
+                sl[q] = lds_bf16(sa + q * 128);
+                sh[q] = lds_bf16(sa + q * 128 + 16);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (nt * 8 >= s.n) break;
+                uint32_t b[PL][2][4];
+#pragma unroll
+                for (int pl = 0; pl < PL; ++pl) {
+                    ldmatrix4(st + xrow[nt][pl], b[pl][0]);
+                    ldmatrix4(st + xrow[nt][pl] + 64, b[pl][1]);
+                }
+#pragma unroll
+                for (int q = 0; q < 128 / S::GG; ++q) {
+                    int g[PL][4];
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl)
+                        g[pl][0] = g[pl][1] = g[pl][2] = g[pl][3] = 0;
+#pragma unroll
+                    for (int u = q * (S::GG / 32); u < (q + 1) * (S::GG / 32); ++u)
+#pragma unroll
+                        for (int pl = 0; pl < PL; ++pl)
+                            imma_codes(g[pl], w[2 * u], w[2 * u + 1], b[pl][u / 2][2 * (u & 1)],
+                                       b[pl][u / 2][2 * (u & 1) + 1]);
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl) {
+                        acc[nt][pl][0] = fmaf(small_int(g[pl][0]), sl[q], acc[nt][pl][0]);
+                        acc[nt][pl][1] = fmaf(small_int(g[pl][1]), sl[q], acc[nt][pl][1]);
+                        acc[nt][pl][2] = fmaf(small_int(g[pl][2]), sh[q], acc[nt][pl][2]);
+                        acc[nt][pl][3] = fmaf(small_int(g[pl][3]), sh[q], acc[nt][pl][3]);
+                    }
+                }
+            }
+        }
+        c.done();
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (!PACKED) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                acc[nt][0][q] = fmaf(acc[nt][PL - 1][q], 65536.f,
+                                     fmaf(acc[nt][PL / 2][q], 256.f, acc[nt][0][q]));
+        }
+        float* q = red + nt * 160 + 2 * (lane & 3) * 20 + (lane >> 2);
+        q[0] = acc[nt][0][0];
+        q[20] = acc[nt][0][1];
+        q[8] = acc[nt][0][2];
+        q[28] = acc[nt][0][3];
+    }
+}
+
+// Second half, bf16: this warp's 16 rows (of 256 from r0) by the part's share of
+// one expert.  out: its row of the first token at the lane's row of the tile.
+template <int TT>
+__device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool mine, uint32_t hs,
+                                          float* out) {
+    using S = Shape<0, TT>;
+    constexpr int NT = S::NT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
+    const int lm = lane & 7, lq = lane >> 3;
+    // H fragments: matrices (high, k), (high, k + 8), (low, k), (low, k + 8); one
+    // chain of products for each part
+    uint32_t hrow[NT];
+    float acc[NT][4], low[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        hrow[nt] = hs + (lq >> 1) * S::HPART + min(nt * 8 + lm, s.n - 1) * S::HPITCH +
+                   (s.hb + (lq & 1) * 8) * 2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[nt][q] = low[nt][q] = 0.f;
+    }
+    for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
+        const int np = min(S::PANELS, s.len / 32 - p0);
+        const uint32_t st = smem_addr(c.wait());
+        if (!c.lost && mine) {
+#pragma unroll
+            for (int q = 0; q < S::PANELS; ++q) {
+                if (q >= np) break;
+                // box (q, rb): 128 rows of 64 bytes
+                const uint32_t wa =
+                    st + (q * 2 + rb) * S::ROWBLK + (tile * 16 + (lq & 1) * 8 + lm) * 64;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t f[4];
+                    ldmatrix4(wa + (((u * 2 + (lq >> 1)) ^ ((lm >> 1) & 3)) << 4), f);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt * 8 < s.n) {
+                            uint32_t b[4];
+                            ldmatrix4(hrow[nt] + (p0 + q) * 64 + u * 32, b);
+                            mma(acc[nt], f, b[0], b[1]);
+                            mma(low[nt], f, b[2], b[3]);
+                        }
+                }
+            }
+        }
+        c.done();
+    }
+    if (mine) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int n = nt * 8 + 2 * (lane & 3);
+            float* q = out + (int64_t)n * d;
+            if (n < s.n) {
+                q[0] = acc[nt][0] + low[nt][0];
+                q[8] = acc[nt][2] + low[nt][2];
+            }
+            if (n + 1 < s.n) {
+                q[d] = acc[nt][1] + low[nt][1];
+                q[d + 8] = acc[nt][3] + low[nt][3];
+            }
+        }
+    }
+}
+
+// The same for 4 bits.  hf: what the planes of H are multiplied by, per token.
+template <int G, int TT, bool PACKED>
+__device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool mine, uint32_t hs,
+                                        const float* hf, float* out) {
+    using S = Shape<G, TT>;
+    constexpr int NT = PACKED ? 1 : S::NT, PL = PACKED ? 1 : 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
+    const int lm = lane & 7, lq = lane >> 3, ft = lane & 3;
+    uint32_t hrow[NT][PL];
+    float acc[NT][PL][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl) {
+            const int col = min(lm, 3 * s.n - 1);  // packed: (token, plane)
+            const int n = PACKED ? col / 3 : min(nt * 8 + lm, s.n - 1);
+            hrow[nt][pl] = hs + n * S::HPITCH + (PACKED ? col % 3 : pl) * S::HPLANE + s.hb + lq * 16;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[nt][pl][q] = 0.f;
+        }
+    for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
+        const int np = min(S::PANELS, s.len / 32 - p0);
+        const uint8_t* stp = c.wait();
+        if (!c.lost && mine) {
+            const int first = s.j0 / 32 + p0, q0 = first * 32 / S::GG;
+            const uint2* cw = reinterpret_cast<const uint2*>(stp + rb * S::ROWBLK + tile * 256) + lane;
+            const uint32_t sa = smem_addr(stp) + S::SCALES + rb * S::GROUPS * 256 +
+                                (tile * 16 + (lane >> 2)) * 2;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (nt * 8 >= s.n) break;
+                int g[PL][4];
+#pragma unroll
+                for (int pl = 0; pl < PL; ++pl) g[pl][0] = g[pl][1] = g[pl][2] = g[pl][3] = 0;
+#pragma unroll
+                for (int q = 0; q < S::PANELS; q += 2) {  // H fragments serve two panels
+                    if (q >= np) break;
+                    uint32_t b[PL][4];
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl) ldmatrix4(hrow[nt][pl] + (p0 + q) * 32, b[pl]);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (q + half >= np) break;
+                        const uint2 w = cw[(q + half) * 256];
+#pragma unroll
+                        for (int pl = 0; pl < PL; ++pl)
+                            imma_codes(g[pl], w.x, w.y, b[pl][2 * half], b[pl][2 * half + 1]);
+                        // the group ends, or the stage
+                        const int at = first + q + half;
+                        if (S::GG == 32 || (at + 1) * 32 % S::GG == 0 || q + half == np - 1) {
+                            const uint32_t sq = sa + (at * 32 / S::GG - q0) * 256;
+                            const float sl = lds_bf16(sq), sh = lds_bf16(sq + 16);
+#pragma unroll
+                            for (int pl = 0; pl < PL; ++pl) {
+                                acc[nt][pl][0] = fmaf(small_int(g[pl][0]), sl, acc[nt][pl][0]);
+                                acc[nt][pl][1] = fmaf(small_int(g[pl][1]), sl, acc[nt][pl][1]);
+                                acc[nt][pl][2] = fmaf(small_int(g[pl][2]), sh, acc[nt][pl][2]);
+                                acc[nt][pl][3] = fmaf(small_int(g[pl][3]), sh, acc[nt][pl][3]);
+                                g[pl][0] = g[pl][1] = g[pl][2] = g[pl][3] = 0;
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        c.done();
+    }
+    if (!mine) return;
+    if (PACKED) {
+        // columns 2 ft, 2 ft + 1 of (token 0: planes 0, 1, 2; token 1: planes 0, 1, 2)
+        const float w0 = ft == 1 ? 65536.f : 1.f, w1 = ft == 1 ? 1.f : 256.f;
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+            const float p = acc[0][0][2 * hi], q = acc[0][0][2 * hi + 1];
+            const float t0 = ft == 0 ? fmaf(q, w1, p) : ft == 1 ? p * w0 : 0.f;
+            const float t1 = ft == 1 ? q : ft == 2 ? fmaf(q, 65536.f, p * 256.f) : 0.f;
+            const float y0 = quad_sum(t0), y1 = quad_sum(t1);
+            if (ft == 0) out[8 * hi] = y0 * hf[0];
+            if (ft == 1 && s.n > 1) out[(int64_t)d + 8 * hi] = y1 * hf[1];
+        }
+        return;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float y[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            y[q] = fmaf(acc[nt][PL - 1][q], 65536.f, fmaf(acc[nt][PL / 2][q], 256.f, acc[nt][0][q]));
+        const int n = nt * 8 + 2 * ft;
+        float* q = out + (int64_t)n * d;
+        if (n < s.n) {
+            q[0] = y[0] * hf[n];
+            q[8] = y[2] * hf[n];
+        }
+        if (n + 1 < s.n) {
+            q[d] = y[1] * hf[n + 1];
+            q[d + 8] = y[3] * hf[n + 1];
+        }
+    }
+}
+
+// v 2^e as three signed digits of 8 bits, low first (|v 2^e| < 2^22).
+__device__ __forceinline__ void digits(float scaled, int8_t (&p)[3]) {
+    int v = __float2int_rn(scaled);
+    p[0] = (int8_t)v;
+    v = (v - p[0]) >> 8;
+    p[1] = (int8_t)v;
+    p[2] = (int8_t)((v - p[1]) >> 8);
+}
+
+// Exponent e that brings magnitudes up to m (finite) below 2^22.
+__device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? 21 - ilogbf(m) : 0; }
+
+template <int G, int TT>
+__device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring, int slot,
+                        int stages, uint64_t* full, uint64_t* empty, uint8_t* Hs, float* red,
+                        float (*hf)[FT], int32_t* flags) {
+    using S = Shape<G, TT>;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gw = warp >> 2, gt = tid & 127;  // group of four warps; thread of the group
+    const int d = a.d;
+    Consumer c;
+    c.ring = ring;
+    c.full = full;
+    c.empty = empty;
+    c.flags = flags;
+    c.status = a.status;
+    c.limit = a.wait_limit_ns;
+    c.slot = slot;
+    c.p.stages = stages;
+    int turn = 0;  // which half of red
     for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
         named_sync(1, CONSUMERS);  // the last part's shares and H have been read
         if (warp == 0) {
@@ -565,230 +939,123 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
         // ---------------------------------------------------- H
         for (int i = 0; i < nseg; ++i) {
             const Seg s = segs[i];
-            // rows of tokens past the expert's repeat its last one: their columns
-            // of the product are never read
-            uint32_t xrow[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                xrow[nt] = S::XOFF + min(nt * 8 + lm, s.n - 1) * S::XPITCH +
-                           (kw * S::KP + lq * 8) * 2;
-            for (int j = 0; j < s.len; j += FEW_GRAN) {
-                float acc[S::MW][NT][4];
-#pragma unroll
-                for (int m = 0; m < S::MW; ++m)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[m][nt][q] = 0.f;
-                for (int k0 = 0; k0 < d; k0 += S::KA) {
-                    const uint32_t st = wait();
-                    if (!lost && k0 + kw * S::KP < d) {
-                        uint32_t b[NT][S::KP / 32][4];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            if (nt * 8 < s.n) {
-#pragma unroll
-                                for (int q = 0; q < S::KP / 32; ++q)
-                                    ldmatrix4(st + xrow[nt] + q * 64, b[nt][q]);
-                            }
-#pragma unroll
-                        for (int m = 0; m < S::MW; ++m) {
-                            const int g = m * S::GW + gw;
-                            if (S::Q4) {
-                                const uint4* cw = reinterpret_cast<const uint4*>(
-                                    ring + (size_t)p.stage * slot + kw * S::QB + g * 1024);
-                                uint32_t w[8];
-                                *reinterpret_cast<uint4*>(w) = cw[lane];
-                                *reinterpret_cast<uint4*>(w + 4) = cw[32 + lane];
-                                const uint32_t sa = st + kw * S::QB + 4096 + (g * 16 + fg) * 2;
-#pragma unroll
-                                for (int q = 0; q < 128 / S::GG; ++q) {
-                                    float c[NT][4];
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-#pragma unroll
-                                    for (int u = q * (S::GG / 16); u < (q + 1) * (S::GG / 16); ++u) {
-                                        uint32_t f[4];
-                                        codes_to_frag(w[u], f);
-#pragma unroll
-                                        for (int nt = 0; nt < NT; ++nt)
-                                            if (nt * 8 < s.n)
-                                                mma(c[nt], f, b[nt][u / 2][2 * (u & 1)],
-                                                    b[nt][u / 2][2 * (u & 1) + 1]);
-                                    }
-                                    const float sl = lds_bf16(sa + q * 128);
-                                    const float sh = lds_bf16(sa + q * 128 + 16);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        acc[m][nt][0] = fmaf(c[nt][0], sl, acc[m][nt][0]);
-                                        acc[m][nt][1] = fmaf(c[nt][1], sl, acc[m][nt][1]);
-                                        acc[m][nt][2] = fmaf(c[nt][2], sh, acc[m][nt][2]);
-                                        acc[m][nt][3] = fmaf(c[nt][3], sh, acc[m][nt][3]);
-                                    }
-                                }
-                            } else {
-                                // box of this warp's 64 columns: 32 gate rows, 32 up rows
-                                const uint32_t wa = st + kw * 8192 + ((lq & 1) * 32 + g * 8 + lm) * 128;
-#pragma unroll
-                                for (int u = 0; u < S::KP / 16; ++u) {
-                                    uint32_t f[4];
-                                    ldmatrix4(wa + (((u * 2 + (lq >> 1)) ^ lm) << 4), f);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        if (nt * 8 < s.n)
-                                            mma(acc[m][nt], f, b[nt][u / 2][2 * (u & 1)],
-                                                b[nt][u / 2][2 * (u & 1) + 1]);
-                                }
-                            }
-                        }
-                    }
-                    done();
-                }
-                named_sync(1, CONSUMERS);  // the last granule's sums have been read
-#pragma unroll
-                for (int m = 0; m < S::MW; ++m)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float* q = red + ((warp * S::MW + m) * NT + nt) * 160 + 2 * ft * 20 + fg;
-                        q[0] = acc[m][nt][0];
-                        q[20] = acc[m][nt][1];
-                        q[8] = acc[m][nt][2];
-                        q[28] = acc[m][nt][3];
-                    }
-                named_sync(1, CONSUMERS);
-                __nv_bfloat16* H = reinterpret_cast<__nv_bfloat16*>(Hs);
-                if (tid < FEW_GRAN * s.n) {
-                    const int jj = tid & 7, g = (tid >> 3) & 3, n = tid >> 5;
+            const bool packed = S::Q4 && s.n <= 2;
+            const int jj = gt & 7, n = gt >> 3;  // the unit of the group's 8, and the token
+            const float gate = n < s.n ? r.gate[s.item][n] : 0.f;
+            const float xf = S::Q4 && n < s.n ? a.xf[r.tok[s.item][n]] : 1.f;
+            for (int j = 0; j < s.len; j += FEW_GRAN, turn ^= 1) {
+                float* base = red + turn * (S::RED / 8);
+                float* mine = base + warp * (S::NT * 160);
+                if constexpr (!S::Q4)
+                    up_bf16<TT>(c, s, d, mine);
+                else if (TT <= 2 || packed)
+                    up_q4<G, TT, true>(c, s, d, mine);
+                else
+                    up_q4<G, TT, false>(c, s, d, mine);
+                named_sync(2 + gw, 128);
+                if (n < s.n) {
                     float ga = 0.f, up = 0.f;
 #pragma unroll
                     for (int w = 0; w < S::KW; ++w) {
-                        const float* q = red + ((((g % S::GW) * S::KW + w) * S::MW + g / S::GW) * NT +
-                                                n / 8) * 160 + (n & 7) * 20 + jj;
-                        ga += q[0];
-                        up += q[8];
+                        const float* q = base + (gw * 4 + w) * (S::NT * 160) + jj;
+                        if (packed) {
+                            q += 3 * n * 20;
+                            ga += fmaf(q[40], 65536.f, fmaf(q[20], 256.f, q[0]));
+                            up += fmaf(q[48], 65536.f, fmaf(q[28], 256.f, q[8]));
+                        } else {
+                            q += n * 20;  // (a tile of 8 tokens is 160 floats)
+                            ga += q[0];
+                            up += q[8];
+                        }
                     }
-                    const float hv = silu_f(ga) * up * r.gate[s.item][n];
-                    const float hi = bf16_round(hv);
-                    const int at = n * (S::HPITCH / 2) + s.hb + j + g * 8 + jj;
-                    H[at] = __float2bfloat16_rn(hi);
-                    H[S::HPART / 2 + at] = __float2bfloat16_rn(hv - hi);
+                    const int at = s.hb + j + gw * 8 + jj;
+                    const float hv = silu_f(ga * xf) * (up * xf) * gate;
+                    if (S::Q4) {
+                        reinterpret_cast<float*>(Hs + n * S::HPITCH)[at] = hv;
+                    } else {
+                        __nv_bfloat16* H = reinterpret_cast<__nv_bfloat16*>(Hs + n * S::HPITCH);
+                        const float hi = bf16_round(hv);
+                        H[at] = __float2bfloat16_rn(hi);
+                        H[S::HPART / 2 + at] = __float2bfloat16_rn(hv - hi);
+                    }
                 }
             }
         }
         named_sync(1, CONSUMERS);
+        if constexpr (S::Q4) {
+            // a warp turns a token's row into planes, in place
+            if (warp < TT) {
+                const float* row = reinterpret_cast<const float*>(Hs + warp * S::HPITCH);
+                float h[FEW_HCAP / 32];
+#pragma unroll
+                for (int q = 0; q < FEW_HCAP / 32; ++q) h[q] = row[q * 32 + lane];
+                __syncwarp();
+                for (int i = 0; i < nseg; ++i) {
+                    const Seg& s = segs[i];
+                    if (warp >= s.n) continue;
+                    const int p0 = s.hb / 32, p1 = (s.hb + s.len) / 32;
+                    float m = 0.f;
+                    bool odd = false;  // infinities and NaN: the token's output is NaN
+#pragma unroll
+                    for (int q = 0; q < FEW_HCAP / 32; ++q)
+                        if (q >= p0 && q < p1) {
+                            m = fmaxf(m, fabsf(h[q]));
+                            odd |= !(fabsf(h[q]) < INFINITY);
+                        }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    odd = __any_sync(0xffffffffu, odd);
+                    const int e = odd ? 0 : plane_exponent(m);
+                    int8_t* dst = reinterpret_cast<int8_t*>(Hs + warp * S::HPITCH) + lane;
+#pragma unroll
+                    for (int q = 0; q < FEW_HCAP / 32; ++q)
+                        if (q >= p0 && q < p1) {
+                            int8_t pl[3];
+                            digits(odd ? 0.f : scalbnf(h[q], e), pl);
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) dst[k * S::HPLANE + q * 32] = pl[k];
+                        }
+                    if (lane == 0) hf[i][warp] = odd ? NAN : scalbnf(0.0625f, -e);
+                }
+            }
+            named_sync(1, CONSUMERS);
+        }
         // ---------------------------------------------------- this part of the output
+        const uint32_t hs = smem_addr(Hs);
         const int rb = warp >> 3, tile = warp & 7;  // this warp's 16 rows of 256
         for (int r0 = 0; r0 < d; r0 += 256) {
             const bool mine = r0 + rb * 128 < d;
             for (int i = 0; i < nseg; ++i) {
                 const Seg s = segs[i];
-                // one chain of products for each part of H
-                float acc[NT][4], low[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[nt][q] = low[nt][q] = 0.f;
-                // H fragments: matrices (high, k), (high, k + 8), (low, k), (low, k + 8)
-                uint32_t hrow[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    hrow[nt] = hs + (lq >> 1) * S::HPART + min(nt * 8 + lm, s.n - 1) * S::HPITCH +
-                               (s.hb + (lq & 1) * 8) * 2;
-                for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
-                    const int np = min(S::PANELS, s.len / 32 - p0);
-                    const uint32_t st = wait();
-                    if (!lost && mine) {
-                        const int pp = s.j0 / 32 + p0, q0 = pp * 32 / S::GG;
-#pragma unroll 2
-                        for (int c = 0; c < np; ++c) {
-                            uint32_t b[NT][2][4];
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (nt * 8 < s.n) {
-                                    ldmatrix4(hrow[nt] + (p0 + c) * 64, b[nt][0]);
-                                    ldmatrix4(hrow[nt] + (p0 + c) * 64 + 32, b[nt][1]);
-                                }
-                            if (S::Q4) {
-                                const uint2 w = reinterpret_cast<const uint2*>(
-                                    ring + (size_t)p.stage * slot + rb * 16384 +
-                                    (c * 8 + tile) * 256)[lane];
-                                const uint32_t sa = st + S::SCALES +
-                                                    (rb * S::GROUPS + (pp + c) * 32 / S::GG - q0) * 256 +
-                                                    (tile * 16 + fg) * 2;
-                                const float sl = lds_bf16(sa), sh = lds_bf16(sa + 16);
-                                uint32_t f0[4], f1[4];
-                                codes_to_frag(w.x, f0);
-                                codes_to_frag(w.y, f1);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    if (nt * 8 < s.n) {
-                                        float ch[4] = {0.f, 0.f, 0.f, 0.f};
-                                        float cl[4] = {0.f, 0.f, 0.f, 0.f};
-                                        mma(ch, f0, b[nt][0][0], b[nt][0][1]);
-                                        mma(cl, f0, b[nt][0][2], b[nt][0][3]);
-                                        mma(ch, f1, b[nt][1][0], b[nt][1][1]);
-                                        mma(cl, f1, b[nt][1][2], b[nt][1][3]);
-                                        acc[nt][0] = fmaf(ch[0] + cl[0], sl, acc[nt][0]);
-                                        acc[nt][1] = fmaf(ch[1] + cl[1], sl, acc[nt][1]);
-                                        acc[nt][2] = fmaf(ch[2] + cl[2], sh, acc[nt][2]);
-                                        acc[nt][3] = fmaf(ch[3] + cl[3], sh, acc[nt][3]);
-                                    }
-                            } else {
-                                // box (c, rb): 128 rows of 64 bytes
-                                const int row = tile * 16 + (lq & 1) * 8 + lm;
-                                const uint32_t wa = st + (c * 2 + rb) * 8192 + row * 64;
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    uint32_t f[4];
-                                    ldmatrix4(wa + (((u * 2 + (lq >> 1)) ^ ((lm >> 1) & 3)) << 4), f);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        if (nt * 8 < s.n) {
-                                            mma(acc[nt], f, b[nt][u][0], b[nt][u][1]);
-                                            mma(low[nt], f, b[nt][u][2], b[nt][u][3]);
-                                        }
-                                }
-                            }
-                        }
-                    }
-                    done();
-                }
-                if (mine) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int n = nt * 8 + 2 * ft;
-                        float* q = a.part + (int64_t)(s.row + n) * d + r0 + rb * 128 + tile * 16 + fg;
-                        if (n < s.n) {
-                            q[0] = acc[nt][0] + low[nt][0];
-                            q[8] = acc[nt][2] + low[nt][2];
-                        }
-                        if (n + 1 < s.n) {
-                            q[d] = acc[nt][1] + low[nt][1];
-                            q[d + 8] = acc[nt][3] + low[nt][3];
-                        }
-                    }
-                }
+                float* out = a.part + (int64_t)s.row * d + r0 + rb * 128 + tile * 16 + (lane >> 2);
+                if constexpr (!S::Q4)
+                    down_bf16<TT>(c, s, d, mine, hs, out);
+                else if (TT <= 2 || s.n <= 2)
+                    down_q4<G, TT, true>(c, s, d, mine, hs, hf[i], out);
+                else
+                    down_q4<G, TT, false>(c, s, d, mine, hs, hf[i], out);
             }
         }
     }
 }
 
-template <int G, int NT>
+template <int G, int TT>
 __global__ void __launch_bounds__(FFN_THREADS, 1)
     few_ffn_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a,
                    int slot, int stages) {
-    using S = Shape<G, NT>;
+    using S = Shape<G, TT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + (-smem_addr(smem_raw) & 1023);
     uint8_t* Hs = ring + (size_t)slot * stages;
-    float* red = reinterpret_cast<float*>(Hs + 2 * S::HPART);
-    Routing& r = *reinterpret_cast<Routing*>(Hs + 2 * S::HPART + S::RED);
+    float* red = reinterpret_cast<float*>(Hs + (S::HBYTES + 15) / 16 * 16);
+    Routing& r = *reinterpret_cast<Routing*>(reinterpret_cast<uint8_t*>(red) + S::RED);
     uint64_t* full = reinterpret_cast<uint64_t*>(
         reinterpret_cast<uint8_t*>(&r) + (sizeof(Routing) + 15) / 16 * 16);
     uint64_t* empty = full + MAX_STAGES;
-    int32_t* flags = reinterpret_cast<int32_t*>(empty + MAX_STAGES);  // a wait ran out; stages issued; shares of the part
+    // a wait ran out; stages issued; shares of the part
+    int32_t* flags = reinterpret_cast<int32_t*>(empty + MAX_STAGES);
     __shared__ Seg segs[3][MAX_SEGS];
+    __shared__ float hf[MAX_SEGS][FT];
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
@@ -803,16 +1070,16 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         }
     }
     pdl_trigger();
-    pdl_wait();  // the router's logits
+    pdl_wait();  // the router's logits (and planes)
     route_batch(a, r);
     if (a.test_stall && blockIdx.x == 0 && warp >= CONSUMERS / 32) {
         // the test hook: nothing is brought in, the consumers' waits run out
     } else if (warp == CONSUMERS / 32) {
-        bring_weights<G, NT>(a, r, maps, segs[1], ring, slot, stages, full, empty, &flags[1]);
+        bring_weights<G, TT>(a, r, maps, segs[1], ring, slot, stages, full, empty, &flags[1]);
     } else if (warp > CONSUMERS / 32) {
-        bring_tokens<G, NT>(a, r, segs[2], ring, slot, stages, full, empty);
+        bring_tokens<G, TT>(a, r, segs[2], ring, slot, stages, full, empty);
     } else {
-        consume<G, NT>(a, r, segs[0], ring, slot, stages, full, empty, Hs, red, flags);
+        consume<G, TT>(a, r, segs[0], ring, slot, stages, full, empty, Hs, red, hf, flags);
     }
     if (blockIdx.x == gridDim.x - 1) publish_routing(a, r);
     __syncthreads();
@@ -876,44 +1143,95 @@ __global__ void __launch_bounds__(256) few_combine_kernel(const __grid_constant_
 // eighth of d; the blocks' sums meet in the first one through its cluster's
 // shared memory, in block order.  W_r is read once whatever T, and even E = 8
 // spreads over 8 SMs, where one block per token took the latency of reading
-// the whole of W_r in turn.
+// the whole of W_r in turn.  With 4-bit weights one more cluster turns x into
+// planes (see the expert kernel).
 constexpr int RC = 8;
+constexpr int ROUTER_THREADS = 256;
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t caddr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(caddr) : "memory");
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
     return v;
 }
 
-template <int TT>
-__global__ void __cluster_dims__(1, RC, 1) __launch_bounds__(256)
-    few_router_kernel(const __nv_bfloat16* __restrict__ x, const float* __restrict__ Wr,
-                      float* __restrict__ z, int T, int d, int E, int32_t* status) {
-    constexpr int N = TT * 8;
-    __shared__ float part[8][N];
-    __shared__ float sum[N];
+// Planes of this block's eighth of every token's row; xf[t] is what their sum is
+// multiplied by.  Rows with an infinity or NaN get zeros and the factor NaN.
+__device__ void split_planes(const FewArgs& a) {
+    __shared__ uint32_t top[FT];  // bits of the largest magnitude: ordered as unsigned
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int e0 = blockIdx.x * 8, len = d / RC, c0 = blockIdx.y * len;
+    const int d = a.d, len = d / RC, c0 = blockIdx.y * len;
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
+    for (int t = warp; t < a.T; t += ROUTER_THREADS / 32) {
+        uint32_t m = 0;
+        for (int c = lane; c < len; c += 32) m = max(m, x[(int64_t)t * d + c0 + c] & 0x7FFFu);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) top[t] = m;
+    }
+    cluster_sync_all();
+    for (int t = warp; t < a.T; t += ROUTER_THREADS / 32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < RC; ++q) m = max(m, ld_cluster_u32(map_shared_rank(smem_addr(&top[t]), q)));
+        const bool odd = m >= 0x7F80u;
+        const int e = odd ? 0 : plane_exponent(__uint_as_float(m << 16));
+        int8_t* dst = a.xq + (int64_t)t * 3 * d + c0;
+        for (int c = lane; c < len; c += 32) {
+            const float v = __uint_as_float((uint32_t)x[(int64_t)t * d + c0 + c] << 16);
+            int8_t p[3];
+            digits(odd ? 0.f : scalbnf(v, e), p);
+#pragma unroll
+            for (int q = 0; q < 3; ++q) dst[(int64_t)q * d + c] = p[q];
+        }
+        // the codes come as 16 q
+        if (lane == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(0.0625f, -e);
+    }
+    cluster_sync_all();  // the maxima are read before their blocks go
+}
+
+// VEC: rows of W_r are read 16 bytes at a time (E a multiple of 4).
+template <int TT, bool VEC>
+__global__ void __cluster_dims__(1, RC, 1) __launch_bounds__(ROUTER_THREADS)
+    few_router_kernel(const __grid_constant__ FewArgs a, const float* __restrict__ Wr,
+                      float* __restrict__ z) {
+    constexpr int N = TT * 4;
+    __shared__ float part[ROUTER_THREADS / 32][TT * 8];
+    __shared__ float sum[TT * 8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int d = a.d, E = a.E, T = a.T;
     pdl_trigger();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *status = DEV_OK;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *a.status = DEV_OK;
+    if ((int)blockIdx.x == (E + 7) / 8) {
+        split_planes(a);
+        return;
+    }
+    // two lanes share a row of W_r: four experts each
+    const int len = d / RC, c0 = blockIdx.y * len, e0 = blockIdx.x * 8 + (tid & 1) * 4;
+    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(a.x);
     float v[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.f;
-    for (int c = c0 + tid; c < c0 + len; c += 256) {
-        float w[8];
+#pragma unroll 4
+    for (int c = c0 + tid / 2; c < c0 + len; c += ROUTER_THREADS / 2) {
+        float w[4];
+        if (VEC) {
+            const float4 f = e0 < E ? *reinterpret_cast<const float4*>(Wr + (int64_t)c * E + e0)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[0] = f.x; w[1] = f.y; w[2] = f.z; w[3] = f.w;
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = e0 + e < E ? Wr[(int64_t)c * E + e0 + e] : 0.f;
+            for (int e = 0; e < 4; ++e) w[e] = e0 + e < E ? Wr[(int64_t)c * E + e0 + e] : 0.f;
+        }
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
             const float xv = t < T ? __bfloat162float(x[(int64_t)t * d + c]) : 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[t * 8 + e] = fmaf(xv, w[e], v[t * 8 + e]);
+            for (int e = 0; e < 4; ++e) v[t * 4 + e] = fmaf(xv, w[e], v[t * 4 + e]);
         }
     }
-    // the warp's sums: each exchange halves the values a lane keeps
-    int n = N, first = 0;
+    // sums over the lanes of one parity: each exchange halves the values a lane keeps
+    int n = N, first = 0, same = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = 16; o > 1; o >>= 1) {
         if (n > 1) {
             n /= 2;
             const bool up = lane & o;
@@ -926,42 +1244,55 @@ __global__ void __cluster_dims__(1, RC, 1) __launch_bounds__(256)
             if (up) first += n;
         } else {
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+            same |= o;
         }
     }
-    constexpr int LEFT = N >= 32 ? N / 32 : 1;
-    if (N >= 32 || (lane & (32 / N - 1)) == 0) {
+    constexpr int LEFT = N >= 16 ? N / 16 : 1;
+    if ((lane & same) == 0) {
 #pragma unroll
-        for (int i = 0; i < LEFT; ++i) part[warp][first + i] = v[i];
+        for (int i = 0; i < LEFT; ++i) {
+            const int q = first + i;  // token q / 4, expert q % 4 of this lane's four
+            part[warp][q / 4 * 8 + (lane & 1) * 4 + q % 4] = v[i];
+        }
     }
     __syncthreads();
-    if (tid < N) {
+    for (int i = tid; i < TT * 8; i += ROUTER_THREADS) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) s += part[w][tid];
-        sum[tid] = s;
+        for (int w = 0; w < ROUTER_THREADS / 32; ++w) s += part[w][i];
+        sum[i] = s;
     }
     cluster_sync_all();
-    if (cluster_ctarank() == 0 && tid < N) {
-        const uint32_t at = smem_addr(&sum[tid]);
-        float s = 0.f;
+    if (cluster_ctarank() == 0)
+        for (int i = tid; i < TT * 8; i += ROUTER_THREADS) {
+            const uint32_t at = smem_addr(&sum[i]);
+            float s = 0.f;
 #pragma unroll
-        for (int q = 0; q < RC; ++q) s += ld_cluster_f32(map_shared_rank(at, q));
-        const int t = tid / 8, e = e0 + tid % 8;
-        if (t < T && e < E) z[(int64_t)t * E + e] = s;
-    }
+            for (int q = 0; q < RC; ++q) s += __uint_as_float(ld_cluster_u32(map_shared_rank(at, q)));
+            const int t = i / 8, e = blockIdx.x * 8 + i % 8;
+            if (t < T && e < E) z[(int64_t)t * E + e] = s;
+        }
     cluster_sync_all();  // the sums are read before their blocks go
 }
 
-template <int G, int NT>
+template <int TT>
+void router_launch(const FewArgs& a, const float* Wr, float* z, cudaStream_t st) {
+    const dim3 grid((a.E + 7) / 8 + (a.G > 0), RC);
+    if (a.E % 4 == 0) few_router_kernel<TT, true><<<grid, ROUTER_THREADS, 0, st>>>(a, Wr, z);
+    else few_router_kernel<TT, false><<<grid, ROUTER_THREADS, 0, st>>>(a, Wr, z);
+}
+
+template <int G, int TT>
 int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
-    using S = Shape<G, NT>;
+    using S = Shape<G, TT>;
     const int slot = S::slot(a.T);
     // the kernel's few static bytes count too
-    const size_t limit = (size_t)smem_limit - 3 * MAX_SEGS * sizeof(Seg) - 256;
+    const size_t limit =
+        (size_t)smem_limit - 3 * MAX_SEGS * sizeof(Seg) - MAX_SEGS * FT * sizeof(float) - 256;
     int stages = (int)((limit - S::fixed()) / slot);
     stages = stages > MAX_STAGES ? MAX_STAGES : stages;
     const size_t smem = S::fixed() + (size_t)slot * stages;
-    auto kern = few_ffn_kernel<G, NT>;
+    auto kern = few_ffn_kernel<G, TT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) !=
         cudaSuccess)
         return launch_result();
@@ -970,14 +1301,11 @@ int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t 
     return launch_result();
 }
 
-template <int NT>
-int launch_ffn_group(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
-    switch (a.G) {
-        case 0: return launch_ffn<0, NT>(m, a, smem_limit, st);
-        case 32: return launch_ffn<32, NT>(m, a, smem_limit, st);
-        case 64: return launch_ffn<64, NT>(m, a, smem_limit, st);
-        default: return launch_ffn<128, NT>(m, a, smem_limit, st);
-    }
+template <int G>
+int launch_ffn_tokens(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
+    if (G && a.T <= 2) return launch_ffn<G, G ? 2 : 8>(m, a, smem_limit, st);
+    if (a.T <= 8) return launch_ffn<G, 8>(m, a, smem_limit, st);
+    return launch_ffn<G, 16>(m, a, smem_limit, st);
 }
 
 }  // namespace
@@ -996,20 +1324,22 @@ int64_t few_part_rows(int T, int h, int E, int k, int hsum) {
     return most;
 }
 
-int launch_few_router(const void* x, const float* Wr, float* z, int T, int d, int E,
-                      int32_t* status, cudaStream_t st) {
-    const dim3 grid((E + 7) / 8, RC);
-    const __nv_bfloat16* xb = reinterpret_cast<const __nv_bfloat16*>(x);
-    if (T == 1) few_router_kernel<1><<<grid, 256, 0, st>>>(xb, Wr, z, T, d, E, status);
-    else if (T <= 4) few_router_kernel<4><<<grid, 256, 0, st>>>(xb, Wr, z, T, d, E, status);
-    else few_router_kernel<16><<<grid, 256, 0, st>>>(xb, Wr, z, T, d, E, status);
+int launch_few_router(const FewArgs& a, const float* Wr, float* z, cudaStream_t st) {
+    if (a.T == 1) router_launch<1>(a, Wr, z, st);
+    else if (a.T <= 4) router_launch<4>(a, Wr, z, st);
+    else if (a.T <= 8) router_launch<8>(a, Wr, z, st);
+    else router_launch<16>(a, Wr, z, st);
     note_launch();
     return launch_result();
 }
 
 int launch_few_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
-    return a.T <= 8 ? launch_ffn_group<1>(m, a, smem_limit, st)
-                    : launch_ffn_group<2>(m, a, smem_limit, st);
+    switch (a.G) {
+        case 0: return launch_ffn_tokens<0>(m, a, smem_limit, st);
+        case 32: return launch_ffn_tokens<32>(m, a, smem_limit, st);
+        case 64: return launch_ffn_tokens<64>(m, a, smem_limit, st);
+        default: return launch_ffn_tokens<128>(m, a, smem_limit, st);
+    }
 }
 
 int launch_few_combine(const FewArgs& a, cudaStream_t st) {

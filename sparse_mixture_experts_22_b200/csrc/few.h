@@ -18,22 +18,21 @@ constexpr int FEW_HCAP = 512;       // hidden units a part holds in shared memor
 // ---------------------------------------------------------------- 4-bit layout
 //
 // A set is n experts (the routed ones, or the fused shared one) of hidden width
-// hid and model width d; weights are codes q in [-7, 7] stored as q + 8 and one
-// bf16 scale per group of G along the reduction.  Codes sit in the order in
-// which a warp's lanes take them as A fragments (m16 x k16, lane 4g + t): one
-// 32-bit word holds a lane's eight codes of one k16 step, nibble i (0..3) the
-// first and nibble i + 4 the second element of fragment register i, where
-// registers 0 and 2 are row g, 1 and 3 row g + 8, at k = 2t, 2t + 1 (registers
-// 0, 1) and 2t + 8, 2t + 9 (registers 2, 3).
+// hid and model width d; weights are codes q in [-7, 7] in two's complement and
+// one bf16 scale per group of G along the reduction.  Codes sit in the order in
+// which a warp's lanes take them as A fragments of the 8-bit products (m16 x
+// k32, lane 4g + t): one 32-bit word holds a lane's eight codes of 16 columns, in
+// byte i the code of row g (high nibble) and of row g + 8 (low nibble) at column
+// 4t + i.  A nibble in the high half of a byte is 16 q as it lies.
 //
 // Q13: blocks [n][hid/32][d/128] of 64 rows x 128 of d: four tiles of 16 rows
 //      (tile i the gate rows of hidden units 8i..8i+7 of the 32, then their up
-//      rows), each [2][32 lanes][4 words] with k16 step = 4 * half + word; then
-//      the scales [128/G][64 rows] bf16.  The columns of one granule follow one
-//      another, so a stage of any depth is one copy.
+//      rows), each [2][32 lanes][4 words] with 16-column step = 4 * half + word;
+//      then the scales [128/G][64 rows] bf16.  The columns of one granule follow
+//      one another, so a stage of any depth is one copy.
 // Q2:  codes [n][d/128][hid/32][8 row tiles][32 lanes][2 words]: 128 rows of d x
-//      32 hidden units, tile i its rows 16i..16i+15, word = k16 step; then the
-//      scales [n][d/128][hid/G][128 rows] bf16.
+//      32 hidden units, tile i its rows 16i..16i+15, word = 16-column step; then
+//      the scales [n][d/128][hid/G][128 rows] bf16.
 __host__ __device__ constexpr int q13_block_bytes(int G) { return 4096 + 128 * (128 / G); }
 __host__ __device__ inline size_t q13_bytes(int64_t n, int hid, int d, int G) {
     return (size_t)n * (hid / 32) * (d / 128) * q13_block_bytes(G);
@@ -64,6 +63,8 @@ __host__ __device__ inline int few_parts(int64_t tot, int ctas) {
 
 struct FewArgs {
     const void* x;              // [T][d] bf16
+    int8_t* xq;                 // 4 bits: [T][3][d] planes of x, and
+    float* xf;                  // [T] what they are multiplied by (few_router writes both)
     const float* logits;        // [T][E] router logits without bias
     const float* bias;          // [E] or null
     // routed and shared weights: packed bf16, or codes (scales follow them)
@@ -88,9 +89,9 @@ struct FewArgs {
 
 // Upper bound on the rows of FewArgs::part for any routing of the batch.
 int64_t few_part_rows(int T, int h, int E, int k, int hsum);
-// Logits z [T][E] = x Wr; also clears the status word.
-int launch_few_router(const void* x, const float* Wr, float* z, int T, int d, int E,
-                      int32_t* status, cudaStream_t st);
+// Logits z [T][E] = x Wr; clears the status word; with 4-bit weights (a.G) also
+// splits x into its planes.
+int launch_few_router(const FewArgs& a, const float* Wr, float* z, cudaStream_t st);
 // Tensor maps of the bf16 weights (unused with 4 bits): W13 as [blocks of 128
 // rows][128][d] in boxes of 64 columns x 32 rows x 2 blocks (a granule's gate
 // and up rows) with the 128-byte swizzle, W2p as rows of the hidden width in

@@ -29,57 +29,60 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
-// Codes of eight weights, nibble e = q + 8 of element e.  q = rint(w / s) without
-// eight divisions: w inv is within 2^-20 of the quotient, and as w and s have 8
-// significant bits and |w / s| <= 7.03, the quotient is either n + 1/2 exactly or
-// at least 2^-10 away from it; the exact remainder tells the half and sends it
-// to the even code.
+// Codes of eight weights, nibble e = q of element e in two's complement.  q =
+// rint(w / s) without eight divisions: w inv is within 2^-20 of the quotient, and
+// as w and s have 8 significant bits and |w / s| <= 7.03, the quotient is either
+// n + 1/2 exactly or at least 2^-10 away from it; the exact remainder tells the
+// half and sends it to the even code.
 __device__ __forceinline__ uint32_t codes_of(const float* w, float s) {
     uint32_t out = 0;
     if (s >= 1.1754944e-38f) {
         const float inv = 1.f / s, half = 0.5f * s;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float q = rintf(w[e] * inv);
+            const float q = rintf(w[e] * inv);
             const float rest = fmaf(-q, s, w[e]);
             int code = (int)q;
             if (fabsf(rest) == half && (code & 1)) code += rest > 0.f ? 1 : -1;
-            out |= (uint32_t)(min(max(code, -7), 7) + 8) << (4 * e);
+            out |= (uint32_t)(min(max(code, -7), 7) & 15) << (4 * e);
         }
     } else {  // no scale, or one below the normal range
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float q = s > 0.f ? rintf(w[e] / s) : 0.f;
-            out |= (uint32_t)((int)fminf(fmaxf(q, -7.f), 7.f) + 8) << (4 * e);
+            out |= (uint32_t)((int)fminf(fmaxf(q, -7.f), 7.f) & 15) << (4 * e);
         }
     }
     return out;
 }
 
+// Four nibbles (bits 0..15) to the low halves of four bytes, and back.
+__device__ __forceinline__ uint32_t spread(uint32_t n) {
+    n = (n | n << 8) & 0x00FF00FFu;
+    return (n | n << 4) & 0x0F0F0F0Fu;
+}
+__device__ __forceinline__ uint32_t gather(uint32_t b) {
+    b = (b | b >> 4) & 0x00FF00FFu;
+    return (b | b >> 8) & 0xFFFFu;
+}
+
 // The lanes' codes (lane (half, c): row g + 8 half, columns 8c..) as fragment
-// words: lane (t, s) = 8t + s gets the word of fragment lane 4g + t, k16 step s.
+// words: lane (t, s) = 8t + s gets the word of fragment lane 4g + t, 16-column
+// step s.
 __device__ __forceinline__ uint32_t to_fragment(uint32_t codes) {
-    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7;
-    uint32_t w = 0;
-#pragma unroll
-    for (int reg = 0; reg < 4; ++reg) {
-        const uint32_t c = __shfl_sync(0xffffffffu, codes, (reg & 1) * 16 + 2 * s + (reg >> 1));
-        const uint32_t two = c >> (8 * t);
-        w |= (two & 15u) << (4 * reg) | (two >> 4 & 15u) << (4 * reg + 16);
-    }
-    return w;
+    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7, c = 2 * s + (t >> 1);
+    const uint32_t lo = __shfl_sync(0xffffffffu, codes, c) >> (16 * (t & 1));
+    const uint32_t hi = __shfl_sync(0xffffffffu, codes, 16 + c) >> (16 * (t & 1));
+    return spread(lo & 0xFFFFu) << 4 | spread(hi & 0xFFFFu);
 }
 
 // The other way: fragment words of lanes (t, s) to the eight codes of lane (half, c).
 __device__ __forceinline__ uint32_t from_fragment(uint32_t w) {
-    const int lane = threadIdx.x & 31, reg = 2 * (lane & 1) + (lane >> 4), s = (lane & 15) >> 1;
-    uint32_t codes = 0;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const uint32_t two = __shfl_sync(0xffffffffu, w, 8 * t + s) >> (4 * reg);
-        codes |= (two & 15u) << (8 * t) | (two >> 16 & 15u) << (8 * t + 4);
-    }
-    return codes;
+    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
+    const uint32_t a = __shfl_sync(0xffffffffu, w, 16 * (c & 1) + (c >> 1));
+    const uint32_t b = __shfl_sync(0xffffffffu, w, 16 * (c & 1) + 8 + (c >> 1));
+    const int shift = half ? 0 : 4;
+    return gather(a >> shift & 0x0F0F0F0Fu) | gather(b >> shift & 0x0F0F0F0Fu) << 16;
 }
 
 // 16 rows x 128 columns of bf16 weights at W (ld elements a row; row i and row
@@ -121,7 +124,7 @@ __device__ __forceinline__ void block_pass(__nv_bfloat16* W, int64_t ld, int64_t
             const uint32_t codes = from_fragment(words[g]);
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = (float)((int)(codes >> (4 * e) & 15u) - 8) * s[g];
+            for (int e = 0; e < 8; ++e) v[e] = (float)((int)(codes << (28 - 4 * e)) >> 28) * s[g];
             uint4 o;
             o.x = pack_bf16x2(v[0], v[1]);
             o.y = pack_bf16x2(v[2], v[3]);

@@ -12,6 +12,14 @@ bound[t][c] adds up, per element:
                                      adds truncate: one 2^-23 each), du alike
   n_h 2^-23 sum |g H w2|             the down sum, in steps of 16 with two parts
                                      each (n_h = 2 h / 16 + parts)
+
+With 4-bit weights the products and the sums of a group are exact, and x and H are
+integers times a power of two instead: of a row of x, the largest magnitude lies
+in [2^21, 2^22) units, so that rounding moves an element by half a unit, 2^-22 of
+the largest at most; of g H the same within an expert's share of a part.  So
+      dx = 2^-22 max |x|,  da gains dx sum |w1|,  du likewise
+      dH = 2^-22 max |H|             in place of 2^-17 |H|
+(both bounds are kept, added up: the sums over groups are in fp32 as before).
 """
 
 import torch
@@ -29,23 +37,25 @@ def quantize(w, group):
     return q.flatten(-2), s.squeeze(-1), (q.double() * s.double()).flatten(-2)
 
 
-def _ffn(x, w1, w3, w2, g):
+def _ffn(x, w1, w3, w2, g, q4):
     """One expert on one token: (g * ffn(x), its bound without the gate's error)."""
     d, h = w1.shape
     a, u = x @ w1, x @ w3
-    da = (d / 16 + 16) * 2.0 ** -23 * (x.abs() @ w1.abs())
-    du = (d / 16 + 16) * 2.0 ** -23 * (x.abs() @ w3.abs())
+    dx = 2.0 ** -22 * x.abs().max() if q4 else 0.0
+    da = (d / 16 + 16) * 2.0 ** -23 * (x.abs() @ w1.abs()) + dx * w1.abs().sum(0)
+    du = (d / 16 + 16) * 2.0 ** -23 * (x.abs() @ w3.abs()) + dx * w3.abs().sum(0)
     s = a * torch.sigmoid(a)
     H = s * u
-    dH = (2.0 ** -17 + 2.0 ** -20) * H.abs() + 1.1 * u.abs() * da + s.abs() * du
+    stored = 2.0 ** -22 * H.abs().max() if q4 else 2.0 ** -17 * H.abs()
+    dH = stored + 2.0 ** -20 * H.abs() + 1.1 * u.abs() * da + s.abs() * du
     y = H @ w2
     dy = dH @ w2.abs() + (2 * h / 16 + 300) * 2.0 ** -23 * (H.abs() @ w2.abs())
     return g * y, g * dy, y.abs()
 
 
-def layer(x, Wr, bias, k, w1, w3, w2, shared=None, cf=None):
+def layer(x, Wr, bias, k, w1, w3, w2, shared=None, cf=None, q4=False):
     """x [T][d]; w1, w3 [E][d][h], w2 [E][h][d] (any float type); shared: (w1s,
-    w3s, w2s) of [S] experts.  Returns a dict with out, bound, idx, gate,
+    w3s, w2s) of [S] experts; q4: bounds of the 4-bit form.  Returns a dict with out, bound, idx, gate,
     routed, kept in fp64 / ints."""
     x, Wr = x.double(), Wr.double()
     T, E = x.shape[0], Wr.shape[1]
@@ -63,11 +73,11 @@ def layer(x, Wr, bias, k, w1, w3, w2, shared=None, cf=None):
             idx[t, j], gate[t, j] = e, p[j]
             routed[e] += 1
             if routed[e] <= C:
-                y, dy, ya = _ffn(x[t], w1[e].double(), w3[e].double(), w2[e].double(), p[j])
+                y, dy, ya = _ffn(x[t], w1[e].double(), w3[e].double(), w2[e].double(), p[j], q4)
                 out[t] += y
                 bound[t] += dy + GATE_ABS * ya
         for s in range(shared[0].shape[0] if shared else 0):
-            y, dy, _ = _ffn(x[t], *(w[s].double() for w in shared), 1.0)
+            y, dy, _ = _ffn(x[t], *(w[s].double() for w in shared), 1.0, q4)
             out[t] += y
             bound[t] += dy
     bound += 2.0 ** -8 * (out.abs() + bound)

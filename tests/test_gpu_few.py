@@ -49,7 +49,7 @@ def made(name, group=0):
             w = {n: F.quantize(v.transpose(1, 2), group)[2].transpose(1, 2) for n, v in w.items()}
         shared = (w["w1s"], w["w3s"], w["w2s"]) if wl.n_shared else None
         ref = F.layer(inp["x"], inp["Wr"], inp["bias"], wl.k, w["w1"], w["w3"], w["w2"], shared,
-                      wl.cf)
+                      wl.cf, group > 0)
         _made[name, group] = (wl, inp, ref)
     return _made[name, group]
 
@@ -332,7 +332,7 @@ def test_prefill_then_decode_from_the_same_4_bits():
     for at in (40, 20, 0):
         x = inp["x"][at:at + 3]
         ref = F.layer(x, inp["Wr"], None, wl.k, w["w1"], w["w3"], w["w2"],
-                      (w["w1s"], w["w3s"], w["w2s"]))
+                      (w["w1s"], w["w3s"], w["w2s"]), None, True)
         F.check(run(layer, x.cuda()), ref)
 
 
