@@ -230,14 +230,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
-// 3-D tiled bulk tensor load (tma_load_2d_hint's, with a third coordinate).
-__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                                 int c0, int c1, int c2, uint64_t policy) {
+// Tiled bulk tensor loads to a shared-memory address.
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap* map,
+                                                 uint64_t* bar, int c0, int c1, int c2,
+                                                 uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2),
         "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap* map,
+                                                 uint64_t* bar, int c0, int c1, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "l"(policy)
         : "memory");
 }
 
@@ -299,10 +309,10 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 
 // ---------------------------------------------------------------- the expert kernel
 //
-// Sixteen warps multiply what two others bring in through a ring of stages:
+// Sixteen warps multiply what four others bring in through a ring of stages:
 // one issues the weights' copies (tensor maps for bf16, bulk copies for 4 bits),
-// the other copies the expert's token rows 16 bytes a lane; both signal the
-// stage's mbarrier.  Weights are the A operand (16 rows), the tokens of one
+// three copy the expert's token rows 16 bytes a lane; all signal the stage's
+// mbarrier.  Weights are the A operand (16 rows), the tokens of one
 // expert the B operand (8 columns a tile), so one instruction takes 256 or 512
 // weights from registers whatever the number of tokens.
 //
@@ -368,7 +378,8 @@ struct Shape {
 
 constexpr int MAX_STAGES = 12;
 constexpr int CONSUMERS = 512;
-constexpr int FFN_THREADS = CONSUMERS + 64;
+constexpr int TOKEN_WARPS = 3;
+constexpr int FFN_THREADS = CONSUMERS + 32 + TOKEN_WARPS * 32;
 constexpr int MAX_SEGS = FEW_HCAP / 128 + 2;  // experts (at least 128 units each) a part can meet
 
 // One expert's share of a part.
@@ -422,142 +433,164 @@ struct Ring {
     }
 };
 
-// Calls up(seg, unit, k0) for every stage of the first half and
-// down(seg, r0, p0, np) for every stage of the second (r0 the first of up to 256
-// rows of d, np panels of 32 units from panel p0 of the share) of all parts of
-// this block, in ring order; a call that returns false ends it.
-template <int G, int TT, typename Up, typename Down>
-__device__ __forceinline__ void for_stages(const FewArgs& a, const Routing& r, Seg* segs, Up up,
-                                           Down down) {
-    using S = Shape<G, TT>;
-    for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
-        const int n = segments(a, r, v, segs);
-        for (int i = 0; i < n; ++i)
-            for (int j = 0; j < segs[i].len; j += FEW_GRAN)
-                for (int k0 = 0; k0 < a.d; k0 += S::KA)
-                    if (!up(segs[i], segs[i].j0 + j, k0)) return;
-        for (int r0 = 0; r0 < a.d; r0 += 256)
-            for (int i = 0; i < n; ++i)
-                for (int p = 0; p < segs[i].len / 32; p += S::PANELS)
-                    if (!down(segs[i], r0, p, min(S::PANELS, segs[i].len / 32 - p))) return;
-    }
-}
+// A bringing warp's side of the ring.
+struct Bringer {
+    uint8_t* ring;
+    uint64_t *full, *empty;
+    uint64_t limit;
+    int slot;
+    Ring p;
 
-// The weights' copies.
+    // Waits until the stage is free; false if the wait ran out (the same in all lanes).
+    __device__ __forceinline__ bool open() {
+        return __all_sync(0xffffffffu, mbar_wait(&empty[p.stage], p.phase ^ 1, limit));
+    }
+    __device__ __forceinline__ uint32_t at() const { return smem_addr(ring) + p.stage * slot; }
+    __device__ __forceinline__ uint64_t* bar() const { return &full[p.stage]; }
+};
+
+// The weights' copies, stage by stage: per part the first half (experts, granules,
+// columns), then the second (experts, 256 rows of d, panels).  False when a wait
+// ran out.
 template <int G, int TT>
-__device__ void bring_weights(const FewArgs& a, const Routing& r, const FewMaps& maps, Seg* segs,
-                              uint8_t* ring, int slot, int stages, uint64_t* full,
-                              uint64_t* empty, int32_t* issued) {
+__device__ __forceinline__ bool bring_weights(const FewArgs& a, const Routing& r,
+                                              const FewMaps& maps, Seg* segs, Bringer c,
+                                              int32_t* issued) {
     using S = Shape<G, TT>;
     const int lane = threadIdx.x & 31;
     const int d = a.d;
     const uint64_t once = l2_policy_evict_first();
-    Ring p;
-    p.stages = stages;
     int count = 0;
-    // waits for the stage to be free and announces its bytes
-    auto open = [&](uint32_t bytes) -> bool {
-        const bool ok = mbar_wait(&empty[p.stage], p.phase ^ 1, a.wait_limit_ns);
-        if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) report_timeout(a.status);
-            return false;
-        }
+    auto announce = [&](uint32_t bytes) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(&full[p.stage], bytes);
+            mbar_arrive_expect_tx(c.bar(), bytes);
             *issued = ++count;
         }
         __syncwarp();
-        return true;
     };
-    auto up = [&](const Seg& s, int j, int k0) -> bool {
-        const bool shared = s.expert < 0;
-        const int hid = shared ? a.hsum : a.h, e = shared ? 0 : s.expert;
-        const int kn = min(S::KA, d - k0);
-        uint8_t* dst = ring + (size_t)p.stage * slot;
-        if (!open(S::Q4 ? kn / 128 * S::QB : kn * 128)) return false;
-        if (S::Q4) {
-            const uint8_t* W = reinterpret_cast<const uint8_t*>(shared ? a.w13s : a.w13);
-            const int64_t blk = ((int64_t)e * (hid / 32) + j / 32) * (d / 128) + k0 / 128;
-            if (lane == 0)
-                bulk_load(smem_addr(dst), W + blk * S::QB, kn / 128 * S::QB, &full[p.stage], once);
-        } else if (lane < kn / 64) {
-            tma_load_3d_hint(dst + lane * 8192, shared ? &maps.w13s : &maps.w13, &full[p.stage],
-                             k0 + lane * 64, j % 128, 2 * (int)(((int64_t)e * hid + j) / 128), once);
+    for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
+        const int nseg = segments(a, r, v, segs);
+        for (int i = 0; i < nseg; ++i) {
+            const Seg s = segs[i];
+            const bool shared = s.expert < 0;
+            const int hid = shared ? a.hsum : a.h, e = shared ? 0 : s.expert;
+            const CUtensorMap* map = shared ? &maps.w13s : &maps.w13;
+            // 4 bits: the granules of a share follow one another
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(shared ? a.w13s : a.w13) +
+                                 ((int64_t)e * (hid / 32) + s.j0 / 32) * (d / 128) * S::QB;
+            int block = 2 * (int)(((int64_t)e * hid + s.j0) / 128), row = s.j0 % 128;
+            for (int j = 0; j < s.len; j += FEW_GRAN) {
+                for (int k0 = 0; k0 < d; k0 += S::KA) {
+                    const int kn = min(S::KA, d - k0);
+                    if (!c.open()) return false;
+                    if (S::Q4) {
+                        const uint32_t bytes = kn / 128 * S::QB;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(c.bar(), bytes);
+                            bulk_load(c.at(), src, bytes, c.bar(), once);
+                            *issued = ++count;
+                        }
+                        src += bytes;
+                    } else {
+                        announce(kn * 128);
+                        if (lane < kn / 64)
+                            tma_load_3d_hint(c.at() + lane * 8192, map, c.bar(), k0 + lane * 64, row,
+                                             block, once);
+                    }
+                    c.p.next();
+                }
+                row += FEW_GRAN;
+                if (row == 128) {
+                    row = 0;
+                    block += 2;
+                }
+            }
         }
-        p.next();
-        return true;
-    };
-    auto down = [&](const Seg& s, int r0, int p0, int np) -> bool {
-        const bool shared = s.expert < 0;
-        const int hid = shared ? a.hsum : a.h, e = shared ? 0 : s.expert;
-        const int nb = min(2, (d - r0) / 128);
-        uint8_t* dst = ring + (size_t)p.stage * slot;
-        if (S::Q4) {
-            const uint8_t* W = reinterpret_cast<const uint8_t*>(shared ? a.w2s : a.w2);
-            const uint8_t* sc = W + q2_code_bytes(shared ? 1 : a.E, hid, d);
-            const int pp = s.j0 / 32 + p0;
-            const int q0 = pp * 32 / S::GG, nq = ((pp + np) * 32 - 1) / S::GG - q0 + 1;
-            if (!open(nb * (np * 2048 + nq * 256))) return false;
-            const int b = lane & 1;
-            const int64_t rb = (int64_t)e * (d / 128) + r0 / 128 + b;
-            if (b < nb && lane < 2)
-                bulk_load(smem_addr(dst) + b * S::ROWBLK, W + (rb * (hid / 32) + pp) * 2048, np * 2048,
-                          &full[p.stage], once);
-            if (b < nb && (lane >> 1) == 1)
-                bulk_load(smem_addr(dst) + S::SCALES + b * S::GROUPS * 256,
-                          sc + (rb * (hid / S::GG) + q0) * 256, nq * 256, &full[p.stage], once);
-        } else {
-            if (!open(nb * np * 8192)) return false;
-            const int b = lane & 1, c = lane >> 1;
-            if (b < nb && c < np)
-                tma_load_2d_hint(dst + lane * 8192, shared ? &maps.w2s : &maps.w2, &full[p.stage],
-                                 s.j0 + (p0 + c) * 32, e * d + r0 + 128 * b, once);
+        for (int i = 0; i < nseg; ++i) {
+            const Seg s = segs[i];
+            const bool shared = s.expert < 0;
+            const int hid = shared ? a.hsum : a.h, e = shared ? 0 : s.expert;
+            const CUtensorMap* map = shared ? &maps.w2s : &maps.w2;
+            // this lane's copy of a stage: block of rows and, for 4 bits, codes (0) or
+            // scales (1), else the panel
+            const int b = lane & 1, what = lane >> 1;
+            const uint8_t* codes = reinterpret_cast<const uint8_t*>(shared ? a.w2s : a.w2);
+            const uint8_t* scales = codes + q2_code_bytes(shared ? 1 : a.E, hid, d);
+            codes += ((int64_t)e * (d / 128) + b) * (hid / 32) * 2048;
+            scales += ((int64_t)e * (d / 128) + b) * (hid / S::GG) * 256;
+            for (int r0 = 0; r0 < d; r0 += 256) {
+                const int nb = min(2, (d - r0) / 128);
+                for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
+                    const int np = min(S::PANELS, s.len / 32 - p0);
+                    const int pp = s.j0 / 32 + p0;
+                    if (!c.open()) return false;
+                    if (S::Q4) {
+                        const int q0 = pp * 32 / S::GG, nq = ((pp + np) * 32 - 1) / S::GG - q0 + 1;
+                        announce(nb * (np * 2048 + nq * 256));
+                        if (b < nb && what < 2)
+                            bulk_load(c.at() + (what ? S::SCALES + b * S::GROUPS * 256 : b * S::ROWBLK),
+                                      what ? scales + q0 * 256 : codes + (int64_t)pp * 2048,
+                                      what ? nq * 256 : np * 2048, c.bar(), once);
+                    } else {
+                        announce(nb * np * 8192);
+                        if (b < nb && what < np)
+                            tma_load_2d_hint(c.at() + lane * 8192, map, c.bar(),
+                                             s.j0 + (p0 + what) * 32, e * d + r0 + 128 * b, once);
+                    }
+                    c.p.next();
+                }
+                codes += (int64_t)2 * (hid / 32) * 2048;
+                scales += (int64_t)2 * (hid / S::GG) * 256;
+            }
         }
-        p.next();
-        return true;
-    };
-    for_stages<G, TT>(a, r, segs, up, down);
+    }
+    return true;
 }
 
-// The token rows of the first half (x, or its planes), 16 bytes a lane; every
-// lane arrives on every stage, when its copies have landed.
+// The token rows of the first half (x, or its planes), 16 bytes a lane, by warp
+// `share` of TOKEN_WARPS; every lane arrives on every stage, when its copies have
+// landed.
 template <int G, int TT>
-__device__ void bring_tokens(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring,
-                             int slot, int stages, uint64_t* full, uint64_t* empty) {
+__device__ __forceinline__ bool bring_tokens(const FewArgs& a, const Routing& r, Seg* segs,
+                                             Bringer c, int share) {
     using S = Shape<G, TT>;
+    static_assert(S::KA * S::XBYTES == 512, "one 16-byte copy of every lane is a row");
     const int lane = threadIdx.x & 31;
-    const uint8_t* x = reinterpret_cast<const uint8_t*>(S::Q4 ? (const void*)a.xq : a.x);
-    Ring p;
-    p.stages = stages;
-    auto open = [&]() -> bool {
-        const bool ok = mbar_wait(&empty[p.stage], p.phase ^ 1, a.wait_limit_ns);
-        return __all_sync(0xffffffffu, ok);
-    };
-    auto up = [&](const Seg& s, int, int k0) -> bool {
-        if (!open()) return false;
-        static_assert(S::KA * S::XBYTES == 512, "one 16-byte copy of every lane is a row");
-        const bool mine = lane * 16 < (a.d - k0) * S::XBYTES;
-        const uint32_t dst = smem_addr(ring + (size_t)p.stage * slot) + S::XOFF + lane * 16;
-        if (mine)
-            for (int n = 0; n < s.n; ++n) {
-                const int64_t row = (int64_t)r.tok[s.item][n] * S::XROWS;
-#pragma unroll
-                for (int q = 0; q < S::XROWS; ++q)
-                    cp_async16(dst + (n * S::XROWS + q) * S::XPITCH,
-                               x + ((row + q) * a.d + k0) * S::XBYTES + lane * 16);
+    const int pitch = a.d * S::XBYTES;  // bytes of a row in memory
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(S::Q4 ? (const void*)a.xq : a.x) + lane * 16;
+    for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
+        const int nseg = segments(a, r, v, segs);
+        for (int i = 0; i < nseg; ++i) {
+            const Seg s = segs[i];
+            const int rows = s.n * S::XROWS;
+            // lane q keeps where this warp's q-th row begins
+            const int mine = share + TOKEN_WARPS * lane;
+            const int64_t at = mine < rows ? ((int64_t)r.tok[s.item][mine / S::XROWS] * S::XROWS +
+                                              mine % S::XROWS) * pitch
+                                           : 0;
+            for (int j = 0; j < s.len; j += FEW_GRAN)
+                for (int k0 = 0; k0 < pitch; k0 += 512) {
+                    if (!c.open()) return false;
+                    const uint32_t dst = c.at() + S::XOFF + lane * 16;
+                    const bool have = k0 + lane * 16 < pitch;
+                    for (int q = 0, row = share; row < rows; ++q, row += TOKEN_WARPS) {
+                        const int64_t from = __shfl_sync(0xffffffffu, at, q);
+                        if (have) cp_async16(dst + row * S::XPITCH, x + from + k0);
+                    }
+                    cp_async_arrive(c.bar());
+                    c.p.next();
+                }
+        }
+        for (int i = 0; i < nseg; ++i) {
+            const int stages = (a.d + 255) / 256 * ((segs[i].len / 32 + S::PANELS - 1) / S::PANELS);
+            for (int q = 0; q < stages; ++q) {
+                if (!c.open()) return false;
+                mbar_arrive(c.bar());
+                c.p.next();
             }
-        cp_async_arrive(&full[p.stage]);
-        p.next();
-        return true;
-    };
-    auto down = [&](const Seg&, int, int, int) -> bool {
-        if (!open()) return false;
-        mbar_arrive(&full[p.stage]);
-        p.next();
-        return true;
-    };
-    for_stages<G, TT>(a, r, segs, up, down);
-    asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+    }
+    return true;
 }
 
 // What a multiplying warp knows of its place and of the ring.
@@ -1023,11 +1056,11 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
         // ---------------------------------------------------- this part of the output
         const uint32_t hs = smem_addr(Hs);
         const int rb = warp >> 3, tile = warp & 7;  // this warp's 16 rows of 256
-        for (int r0 = 0; r0 < d; r0 += 256) {
-            const bool mine = r0 + rb * 128 < d;
-            for (int i = 0; i < nseg; ++i) {
-                const Seg s = segs[i];
-                float* out = a.part + (int64_t)s.row * d + r0 + rb * 128 + tile * 16 + (lane >> 2);
+        for (int i = 0; i < nseg; ++i) {
+            const Seg s = segs[i];
+            float* out = a.part + (int64_t)s.row * d + rb * 128 + tile * 16 + (lane >> 2);
+            for (int r0 = 0; r0 < d; r0 += 256, out += 256) {
+                const bool mine = r0 + rb * 128 < d;
                 if constexpr (!S::Q4)
                     down_bf16<TT>(c, s, d, mine, hs, out);
                 else if (TT <= 2 || s.n <= 2)
@@ -1054,12 +1087,13 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     uint64_t* empty = full + MAX_STAGES;
     // a wait ran out; stages issued; shares of the part
     int32_t* flags = reinterpret_cast<int32_t*>(empty + MAX_STAGES);
-    __shared__ Seg segs[3][MAX_SEGS];
+    __shared__ Seg segs[2 + TOKEN_WARPS][MAX_SEGS];
     __shared__ float hf[MAX_SEGS][FT];
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
-            mbar_init(&full[i], 1 + 32);  // the weights' announcement, the token warp's lanes
+            // the weights' announcement and the token warps' lanes
+            mbar_init(&full[i], 1 + TOKEN_WARPS * 32);
             mbar_init(&empty[i], CONSUMERS / 32);
         }
         flags[0] = flags[1] = 0;
@@ -1072,14 +1106,22 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     pdl_trigger();
     pdl_wait();  // the router's logits (and planes)
     route_batch(a, r);
-    if (a.test_stall && blockIdx.x == 0 && warp >= CONSUMERS / 32) {
-        // the test hook: nothing is brought in, the consumers' waits run out
-    } else if (warp == CONSUMERS / 32) {
-        bring_weights<G, TT>(a, r, maps, segs[1], ring, slot, stages, full, empty, &flags[1]);
-    } else if (warp > CONSUMERS / 32) {
-        bring_tokens<G, TT>(a, r, segs[2], ring, slot, stages, full, empty);
-    } else {
+    if (warp < CONSUMERS / 32) {
         consume<G, TT>(a, r, segs[0], ring, slot, stages, full, empty, Hs, red, hf, flags);
+    } else if (!(a.test_stall && blockIdx.x == 0)) {
+        // (with the test hook nothing is brought in: the consumers' waits run out)
+        Bringer c;
+        c.ring = ring;
+        c.full = full;
+        c.empty = empty;
+        c.limit = a.wait_limit_ns;
+        c.slot = slot;
+        c.p.stages = stages;
+        const int w = warp - CONSUMERS / 32;
+        const bool ok = w == 0 ? bring_weights<G, TT>(a, r, maps, segs[1], c, &flags[1])
+                               : bring_tokens<G, TT>(a, r, segs[1 + w], c, w - 1);
+        if (!ok && (tid & 31) == 0) report_timeout(a.status);
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     if (blockIdx.x == gridDim.x - 1) publish_routing(a, r);
     __syncthreads();
@@ -1288,7 +1330,8 @@ int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t 
     const int slot = S::slot(a.T);
     // the kernel's few static bytes count too
     const size_t limit =
-        (size_t)smem_limit - 3 * MAX_SEGS * sizeof(Seg) - MAX_SEGS * FT * sizeof(float) - 256;
+        (size_t)smem_limit - (2 + TOKEN_WARPS) * MAX_SEGS * sizeof(Seg) -
+        MAX_SEGS * FT * sizeof(float) - 256;
     int stages = (int)((limit - S::fixed()) / slot);
     stages = stages > MAX_STAGES ? MAX_STAGES : stages;
     const size_t smem = S::fixed() + (size_t)slot * stages;
