@@ -14,7 +14,7 @@
 #include "common.cuh"
 #include "few.h"
 #include "kernels.h"
-#include "topk.cuh"
+#include "plan.h"
 
 namespace moe {
 
@@ -25,128 +25,134 @@ constexpr int FT = FEW_MAX_T;
 // The routing of the batch, worked out by every CTA for itself (128
 // assignments at most) in shared memory.
 struct Routing {
+    uint32_t tokens[MAX_E];         // tokens that chose an expert, as bits
+    uint32_t hit[MAX_E / 32];       // experts some token chose, as bits
     int32_t sel[FT * MAX_K];        // [t * k + j] expert
     float g[FT * MAX_K];            // its gate
-    int32_t lead[FT * MAX_K];       // 1: the batch's first assignment to its expert
-    int32_t item_of[FT * MAX_K];    // item of the assignment
-    int32_t pos_of[FT * MAX_K];     // its place in the item's token list, -1 if dropped
     int32_t items;                  // hit experts + the shared one
+    int32_t tot;                    // granules of all items
+    int32_t V;                      // parts
     int32_t expert[FEW_MAX_ITEMS];  // expert of an item, -1: shared
     int32_t n[FEW_MAX_ITEMS];       // tokens it serves
     int32_t row0[FEW_MAX_ITEMS];    // first row of its partial outputs
     uint8_t tok[FEW_MAX_ITEMS][FT];
     float gate[FEW_MAX_ITEMS][FT];
-    int64_t tot;                    // granules of all items
-    int V;                          // parts
 };
 
-// Part that holds granule x (the parts' bounds are v tot / V rounded down).
-__device__ __forceinline__ int part_of(int64_t x, int64_t tot, int V) {
-    return (int)(((x + 1) * V - 1) / tot);
+// First granule of part v, and the part that holds granule x: the first tot % V
+// parts hold one granule more than the others.
+__device__ __forceinline__ int part_start(int v, int tot, int V) {
+    return v * (tot / V) + min(v, tot % V);
+}
+__device__ __forceinline__ int part_of(int x, int tot, int V) {
+    const int q = tot / V, more = tot % V;
+    return x < more * (q + 1) ? x / (q + 1) : more + (x - more * (q + 1)) / q;
 }
 
-__device__ __forceinline__ int64_t item_start(int i, int A, int gE) { return (int64_t)min(i, A) * gE; }
+__device__ __forceinline__ int item_start(int i, int A, int gE) { return min(i, A) * gE; }
 
-// Top-k and gates of one token by one warp: each lane keeps the k best of its
-// experts, k rounds of an arg-max over the lanes' best merge them.
-__device__ void route_token(const FewArgs& a, int t, Routing& r) {
+// Number of hit experts below e.
+__device__ __forceinline__ int hits_below(const Routing& r, int e) {
+    int n = 0;
+    for (int w = 0; w < e >> 5; ++w) n += __popc(r.hit[w]);
+    return n + __popc(r.hit[e >> 5] & ((1u << (e & 31)) - 1));
+}
+
+// fp32 as an unsigned integer of the same order (NaN as -inf, -0 as +0), and back.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint((v != v ? -INFINITY : v) + 0.f);
+    return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Top-k and gates of token t by one warp, C experts a lane at a time: k rounds of
+// a warp-wide maximum over the lanes' keys and, in a lane, what the experts
+// before these left (lane j: the j-th best).  Equal keys go to the lower expert.
+template <int C>
+__device__ __forceinline__ void route_token(const FewArgs& a, int t, Routing& r) {
     const int lane = threadIdx.x & 31;
     const int E = a.E, k = a.k;
     const float* z = a.logits + (int64_t)t * E;
-    float lv[MAX_K];
-    int li[MAX_K];
+    uint32_t best = 0;              // keys of real experts are above 0
+    int expert = 0x7fffffff;
+    for (int e0 = 0; e0 < E; e0 += 32 * C) {
+        uint32_t key[C + 1];
 #pragma unroll
-    for (int j = 0; j < MAX_K; ++j) {
-        lv[j] = -INFINITY;
-        li[j] = -1;
-    }
-    for (int e = lane; e < E; e += 32)
-        topk_insert(lv, li, k, finite_or_minus_inf(a.bias ? z[e] + a.bias[e] : z[e]), e);
-    float vs[MAX_K];
-    int is[MAX_K];
+        for (int i = 0; i < C; ++i) {
+            const int e = e0 + i * 32 + lane;
+            key[i] = e < E ? order_key(a.bias ? z[e] + a.bias[e] : z[e]) : 0u;
+        }
+        key[C] = best;
+        const int kept = expert;
+        best = 0;
+        expert = 0x7fffffff;
+        for (int j = 0; j < k; ++j) {
+            uint32_t m = key[C];
 #pragma unroll
-    for (int j = 0; j < MAX_K; ++j) {
-        vs[j] = -INFINITY;
-        is[j] = 0;
-        if (j >= k) continue;
-        float bv = lv[0];
-        int bi = li[0] < 0 ? 0x7fffffff : li[0];
+            for (int i = 0; i < C; ++i) m = max(m, key[i]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, m);
+            int e = key[C] == top ? kept : 0x7fffffff;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-            const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-            if (ov > bv || (ov == bv && oi < bi)) {
-                bv = ov;
-                bi = oi;
+            for (int i = C - 1; i >= 0; --i)
+                if (key[i] == top) e = min(e, e0 + i * 32 + lane);
+            const int win = (int)__reduce_min_sync(0xffffffffu, (unsigned)e);
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                if (e0 + i * 32 + lane == win) key[i] = 0;
+            if (kept == win) key[C] = 0;
+            if (lane == j) {
+                best = top;
+                expert = win;
             }
         }
-        vs[j] = bv;
-        is[j] = bi;
-        if (li[0] == bi) {
-#pragma unroll
-            for (int q = 0; q < MAX_K - 1; ++q) {
-                lv[q] = lv[q + 1];
-                li[q] = li[q + 1];
-            }
-            lv[MAX_K - 1] = -INFINITY;
-            li[MAX_K - 1] = -1;
-        }
     }
-    float s = 0.f;
+    const float v = key_value(best);
+    const float most = __shfl_sync(0xffffffffu, v, 0);  // by all lanes, outside the choice below
+    const float p = lane < k ? expf(v - most) : 0.f;
+    float sum = p;
 #pragma unroll
-    for (int j = 0; j < MAX_K; ++j)
-        if (j < k) s += expf(vs[j] - vs[0]);
-    if (lane == 0) {
-#pragma unroll
-        for (int j = 0; j < MAX_K; ++j)
-            if (j < k) {
-                r.sel[t * k + j] = is[j];
-                r.g[t * k + j] = expf(vs[j] - vs[0]) / s;
-            }
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane < k) {
+        r.sel[t * k + lane] = expert;
+        r.g[t * k + lane] = p / sum;
+        atomicOr(&r.tokens[expert], 1u << t);
+        atomicOr(&r.hit[expert >> 5], 1u << (expert & 31));
     }
 }
 
 // Fills r: capacity in token order, the hit experts ascending with their
 // tokens and gates, the shared expert last, and the rows of the partial
-// outputs.  Called by every thread of the CTA.
+// outputs.  Called by every thread of the CTA; r.tokens and r.hit are zero.
 __device__ void route_batch(const FewArgs& a, Routing& r) {
-    const int tid = threadIdx.x, nthr = blockDim.x;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int N = a.T * a.k, k = a.k;
-    for (int t = tid >> 5; t < a.T; t += nthr >> 5) route_token(a, t, r);
-    __syncthreads();
-    for (int i = tid; i < N; i += nthr) {
-        int before = 0;
-        for (int b = 0; b < i; ++b) before += r.sel[b] == r.sel[i];
-        r.lead[i] = before == 0;
-        r.pos_of[i] = before < a.C ? before : -1;
+    if (warp < a.T) {
+        if (a.E <= 32) route_token<1>(a, warp, r);
+        else route_token<8>(a, warp, r);
     }
     __syncthreads();
-    for (int i = tid; i < N; i += nthr) {
-        int at = 0, count = 0;
-        for (int b = 0; b < N; ++b) {
-            at += r.lead[b] && r.sel[b] < r.sel[i];
-            count += r.sel[b] == r.sel[i];
+    const int A = hits_below(r, a.E - 1) + (r.tokens[a.E - 1] != 0);
+    const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
+    const int tot = A * gE + gS, V = few_parts(tot, gridDim.x);
+    if (tid < N) {
+        const int e = r.sel[tid], t = tid / k, at = hits_below(r, e);
+        const uint32_t who = r.tokens[e];
+        const int rank = __popc(who & ((1u << t) - 1));
+        if (rank == 0) {
+            r.expert[at] = e;
+            r.n[at] = (int)min((int64_t)__popc(who), a.C);
         }
-        r.item_of[i] = at;
-        if (r.lead[i]) {
-            r.expert[at] = r.sel[i];
-            r.n[at] = (int)min((int64_t)count, a.C);
-        }
-        const int p = r.pos_of[i];
-        if (p >= 0) {
-            r.tok[at][p] = (uint8_t)(i / k);
-            r.gate[at][p] = r.g[i];
+        if (rank < a.C) {
+            r.tok[at][rank] = (uint8_t)t;
+            r.gate[at][rank] = r.g[tid];
         }
     }
-    int A = 0;
-    for (int b = 0; b < N; ++b) A += r.lead[b];
-    if (tid < a.T && a.hsum > 0) {
+    if (gS > 0 && tid < a.T) {
         r.tok[A][tid] = (uint8_t)tid;
         r.gate[A][tid] = 1.0f;
     }
-    const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
-    const int64_t tot = (int64_t)A * gE + gS;
-    const int V = few_parts(tot, gridDim.x);
     if (tid == 0) {
         if (gS) {
             r.expert[A] = -1;
@@ -159,29 +165,22 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
     __syncthreads();
     // exclusive prefix over the items of tokens x parts
     if (tid < 32) {
-        const int per = (FEW_MAX_ITEMS + 31) / 32;
-        int mine = 0;
-        for (int q = 0; q < per; ++q) {
-            const int i = tid * per + q;
+        int before = 0;
+        for (int i0 = 0; i0 < r.items; i0 += 32) {
+            const int i = i0 + tid;
+            int rows = 0;
             if (i < r.items) {
-                const int64_t s = item_start(i, A, gE), e = s + (i < A ? gE : gS);
-                mine += r.n[i] * (part_of(e - 1, tot, V) - part_of(s, tot, V) + 1);
+                const int s = item_start(i, A, gE), e = s + (i < A ? gE : gS);
+                rows = r.n[i] * (part_of(e - 1, tot, V) - part_of(s, tot, V) + 1);
             }
-        }
-        int incl = mine;
+            int incl = rows;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (tid >= o) incl += v;
-        }
-        int at = incl - mine;
-        for (int q = 0; q < per; ++q) {
-            const int i = tid * per + q;
-            if (i < r.items) {
-                const int64_t s = item_start(i, A, gE), e = s + (i < A ? gE : gS);
-                r.row0[i] = at;
-                at += r.n[i] * (part_of(e - 1, tot, V) - part_of(s, tot, V) + 1);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (tid >= o) incl += v;
             }
+            if (i < r.items) r.row0[i] = before + incl - rows;
+            before += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
     __syncthreads();
@@ -194,18 +193,18 @@ __device__ void publish_routing(const FewArgs& a, const Routing& r) {
     const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
     const int A = r.items - (gS > 0);
     for (int e = tid; e < a.E; e += nthr) {
-        int routed = 0;
-        for (int b = 0; b < N; ++b) routed += r.sel[b] == e;
+        const int routed = __popc(r.tokens[e]);
         a.routed[e] = routed;
         a.kept[e] = (int)min((int64_t)routed, a.C);
     }
     for (int i = tid; i < N + a.T; i += nthr) {
         const bool shared = i >= N;
         const int t = shared ? i - N : i / k;
-        const int item = shared ? A : r.item_of[i], pos = shared ? t : r.pos_of[i];
+        const int item = shared ? A : hits_below(r, r.sel[i]);
+        const int pos = shared ? t : __popc(r.tokens[r.sel[i]] & ((1u << t) - 1));
         int4 row = make_int4(0, 0, 0, 0);
-        if (pos >= 0 && !(shared && gS == 0)) {
-            const int64_t s = item_start(item, A, gE), e = s + (shared ? gS : gE);
+        if (shared ? gS > 0 : pos < a.C) {
+            const int s = item_start(item, A, gE), e = s + (shared ? gS : gE);
             row.x = r.row0[item] + pos;
             row.y = part_of(e - 1, r.tot, r.V) - part_of(s, r.tot, r.V) + 1;
             row.z = r.n[item];
@@ -334,8 +333,8 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 // codes -- as bf16 fragments they took three shifts, four masks and four
 // subtractions, and 30 clocks per 256 weights and scheduler against 11, where HBM
 // brings 256 in 23.  Sums within a group are exact in int32; a group's scale
-// multiplies its sum in fp32.  Two tokens' planes fit one tile of 8 columns
-// ("packed"); more take a tile per plane and 8 tokens.
+// multiplies its sum in fp32.  A tile of 8 columns holds the planes of two
+// tokens, two tiles those of five, three those of eight.
 //
 // Copied bf16 tiles are swizzled and token rows pitched by an odd multiple of 16
 // bytes, so that ldmatrix meets no bank twice; codes arrive in fragment order and
@@ -345,7 +344,7 @@ struct Shape {
     static constexpr bool Q4 = G > 0;
     static constexpr int GG = Q4 ? G : 128;
     static constexpr int NT = (TT + 7) / 8;                // tiles of 8 tokens
-    static constexpr int KP = Q4 ? 128 : 64;               // columns of a warp in a stage
+    static constexpr int KP = Q4 ? (TT <= 2 ? 256 : 128) : 64;  // columns of a warp in a stage
     static constexpr int KW = 4;                           // warps along the columns
     static constexpr int KA = KW * KP;                     // columns of a stage
     static constexpr int QB = q13_block_bytes(GG);
@@ -354,15 +353,16 @@ struct Shape {
     static constexpr int XPITCH = KA * XBYTES + 16;
     static constexpr int XOFF = Q4 ? KA / 128 * QB : KA * 128;  // where the tokens begin
     // second half: 2 blocks of 128 rows x panels of 32 units
-    static constexpr int PANELS = Q4 ? (TT <= 2 ? 4 : 8) : 2;
+    static constexpr int PANELS = Q4 ? 8 : 2;
     static constexpr int ROWBLK = Q4 ? PANELS * 2048 : 8192;    // bytes of a block of rows
     static constexpr int SCALES = 2 * PANELS * 2048;            // 4 bits: where its scales begin
     // groups that the panels can meet
     static constexpr int GROUPS = GG == 32 ? PANELS : PANELS * 32 / GG + 1;
     // H: bf16 high then low parts [2][NT * 8][HPITCH]; 4 bits [TT][HPITCH], a row
-    // first fp32, then its three planes HPLANE bytes apart
-    static constexpr int HPLANE = FEW_HCAP + 32;
-    static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 16 : (FEW_HCAP + 8) * 2;
+    // first fp32, then its three planes HPLANE bytes apart (33 and 131 times 16 bytes:
+    // rows of consecutive (token, plane) meet no bank twice)
+    [[maybe_unused]] static constexpr int HPLANE = FEW_HCAP + 16;
+    static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 48 : (FEW_HCAP + 8) * 2;
     static constexpr int HPART = NT * 8 * HPITCH;
     static constexpr int HBYTES = Q4 ? TT * HPITCH : 2 * HPART;
     static constexpr int RED = 2 * 16 * NT * 640;          // the warps' sums, two granules
@@ -390,31 +390,30 @@ struct Seg {
     int hb;                // where its H begins
 };
 
-// Share i of part v (granules g0 .. g1); false past the last one.
-__device__ __forceinline__ bool segment(const FewArgs& a, const Routing& r, int v, int64_t g0,
-                                        int64_t g1, int i, Seg& s) {
+// Share i of part v; false past the last one.
+__device__ __forceinline__ bool segment(const FewArgs& a, const Routing& r, int v, int i, Seg& s) {
     const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
     const int A = r.items - (gS > 0);
-    s.item = (int)min(g0 / gE, (int64_t)A) + i;
+    const int g0 = part_start(v, r.tot, r.V), g1 = part_start(v + 1, r.tot, r.V);
+    s.item = min(g0 / gE, A) + i;
     if (s.item >= r.items) return false;
-    const int64_t is = item_start(s.item, A, gE);
-    const int64_t s0 = max(is, g0), s1 = min(is + (s.item < A ? gE : gS), g1);
+    const int is = item_start(s.item, A, gE);
+    const int s0 = max(is, g0), s1 = min(is + (s.item < A ? gE : gS), g1);
     if (s0 >= s1) return false;
     s.expert = r.expert[s.item];
     s.n = r.n[s.item];
-    s.j0 = (int)(s0 - is) * FEW_GRAN;
-    s.len = (int)(s1 - s0) * FEW_GRAN;
+    s.j0 = (s0 - is) * FEW_GRAN;
+    s.len = (s1 - s0) * FEW_GRAN;
     s.row = r.row0[s.item] + (v - part_of(is, r.tot, r.V)) * s.n;
-    s.hb = (int)(s0 - g0) * FEW_GRAN;
+    s.hb = (s0 - g0) * FEW_GRAN;
     return true;
 }
 
 // A warp writes part v's shares to segs; returns how many there are.
 __device__ __forceinline__ int segments(const FewArgs& a, const Routing& r, int v, Seg* segs) {
     const int lane = threadIdx.x & 31;
-    const int64_t g0 = (int64_t)v * r.tot / r.V, g1 = (int64_t)(v + 1) * r.tot / r.V;
     Seg s;
-    const bool have = lane < MAX_SEGS && segment(a, r, v, g0, g1, lane, s);
+    const bool have = lane < MAX_SEGS && segment(a, r, v, lane, s);
     __syncwarp();
     if (have) segs[lane] = s;
     __syncwarp();
@@ -554,7 +553,7 @@ template <int G, int TT>
 __device__ __forceinline__ bool bring_tokens(const FewArgs& a, const Routing& r, Seg* segs,
                                              Bringer c, int share) {
     using S = Shape<G, TT>;
-    static_assert(S::KA * S::XBYTES == 512, "one 16-byte copy of every lane is a row");
+    constexpr int ROW = S::KA * S::XBYTES;  // bytes of a stage's row
     const int lane = threadIdx.x & 31;
     const int pitch = a.d * S::XBYTES;  // bytes of a row in memory
     const uint8_t* x = reinterpret_cast<const uint8_t*>(S::Q4 ? (const void*)a.xq : a.x) + lane * 16;
@@ -569,13 +568,15 @@ __device__ __forceinline__ bool bring_tokens(const FewArgs& a, const Routing& r,
                                               mine % S::XROWS) * pitch
                                            : 0;
             for (int j = 0; j < s.len; j += FEW_GRAN)
-                for (int k0 = 0; k0 < pitch; k0 += 512) {
+                for (int k0 = 0; k0 < pitch; k0 += ROW) {
                     if (!c.open()) return false;
                     const uint32_t dst = c.at() + S::XOFF + lane * 16;
-                    const bool have = k0 + lane * 16 < pitch;
                     for (int q = 0, row = share; row < rows; ++q, row += TOKEN_WARPS) {
                         const int64_t from = __shfl_sync(0xffffffffu, at, q);
-                        if (have) cp_async16(dst + row * S::XPITCH, x + from + k0);
+#pragma unroll
+                        for (int w = 0; w < ROW; w += 512)
+                            if (k0 + w + lane * 16 < pitch)
+                                cp_async16(dst + row * S::XPITCH + w, x + from + k0 + w);
                     }
                     cp_async_arrive(c.bar());
                     c.p.next();
@@ -619,12 +620,6 @@ struct Consumer {
         p.next();
     }
 };
-
-// Sum of a quad's lanes.
-__device__ __forceinline__ float quad_sum(float v) {
-    v += __shfl_xor_sync(0xffffffffu, v, 1);
-    return v + __shfl_xor_sync(0xffffffffu, v, 2);
-}
 
 // First half, bf16: this warp's sums over d of tile gw's rows by the expert's
 // tokens.  red: where they go, [NT][8 tokens][20] floats.
@@ -679,38 +674,73 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
     }
 }
 
-// The same for 4 bits; packed: the columns are (token, plane), else one tile per
-// plane, joined before they are written.
-template <int G, int TT, bool PACKED>
+// Column c of a tile group of the planes of 8 tokens is token c / 3, plane c % 3:
+// three tiles of 8 columns, of which n tokens use the first 3 n / 8 rounded up.
+__device__ __forceinline__ bool tile_used(int tile, int n) { return tile * 8 < 3 * n; }
+
+// Planes joined: v[tile][4] as the products leave them to y[4], the sums of
+// tokens 2 ft and 2 ft + 1 in the lane's two rows, as a tile of 8 tokens would
+// leave them.  A lane's tokens are columns 6 ft .. 6 ft + 5, in three lanes of a
+// quad; in each round every lane gives one pair of columns and takes one.
+template <int TILES>
+__device__ __forceinline__ void join_planes(const float (&v)[TILES][4], float (&y)[4]) {
+    const int ft = threadIdx.x & 3;
+    float pair[3][4];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        // pair i of lane ft is pair 3 ft + i of the group: tile (3 ft + i) / 4, lane (3 ft
+        // + i) % 4; seen from the giving lane, the tile is
+        int tile = 0;
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+            if ((4 * t + ft - i + 12) % 3 == 0 && 4 * t + ft >= i && (4 * t + ft - i) / 3 < 4) tile = t;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float give = v[0][q];
+#pragma unroll
+            for (int t = 1; t < TILES; ++t) give = tile == t ? v[t][q] : give;
+            if (tile >= TILES) give = 0.f;
+            pair[i][q] = __shfl_sync(0xffffffffu, give, (threadIdx.x & 28) | ((3 * ft + i) & 3));
+        }
+    }
+#pragma unroll
+    for (int hi = 0; hi < 2; ++hi) {
+        y[2 * hi] = fmaf(pair[1][2 * hi], 65536.f, fmaf(pair[0][2 * hi + 1], 256.f, pair[0][2 * hi]));
+        y[2 * hi + 1] =
+            fmaf(pair[2][2 * hi + 1], 65536.f, fmaf(pair[2][2 * hi], 256.f, pair[1][2 * hi + 1]));
+    }
+}
+
+// The same for 4 bits; TILES: tiles of planes per 8 tokens (1: at most two tokens).
+template <int G, int TT, int TILES>
 __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* red) {
     using S = Shape<G, TT>;
-    constexpr int NT = PACKED ? 1 : S::NT, PL = PACKED ? 1 : 3;
+    constexpr int NT = TILES == 1 ? 1 : S::NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
     const int lm = lane & 7, lq = lane >> 3;
-    uint32_t xrow[NT][PL];
+    uint32_t xrow[NT][TILES];
+    float acc[NT][TILES][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int pl = 0; pl < PL; ++pl) {
-            const int row = PACKED ? min(lm, 3 * s.n - 1) : 3 * min(nt * 8 + lm, s.n - 1) + pl;
-            xrow[nt][pl] = S::XOFF + row * S::XPITCH + kw * S::KP + lq * 16;
+        for (int t = 0; t < TILES; ++t) {
+            const int row = min(nt * 24 + t * 8 + lm, 3 * s.n - 1);
+            xrow[nt][t] = S::XOFF + row * S::XPITCH + kw * S::KP + lq * 16;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[nt][t][q] = 0.f;
         }
-    float acc[NT][PL][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int pl = 0; pl < PL; ++pl)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[nt][pl][q] = 0.f;
     for (int k0 = 0; k0 < d; k0 += S::KA) {
         const uint8_t* stp = c.wait();
         const uint32_t st = smem_addr(stp);
-        if (!c.lost && k0 + kw * S::KP < d) {
-            const uint4* cw = reinterpret_cast<const uint4*>(stp + kw * S::QB + gw * 1024);
+#pragma unroll
+        for (int kb = 0; kb < S::KP / 128; ++kb) {
+            if (c.lost || k0 + kw * S::KP + kb * 128 >= d) break;
+            const int blk = kw * (S::KP / 128) + kb;
+            const uint4* cw = reinterpret_cast<const uint4*>(stp + blk * S::QB + gw * 1024);
             uint32_t w[8];
             *reinterpret_cast<uint4*>(w) = cw[lane];
             *reinterpret_cast<uint4*>(w + 4) = cw[32 + lane];
-            const uint32_t sa = st + kw * S::QB + 4096 + (gw * 16 + (lane >> 2)) * 2;
+            const uint32_t sa = st + blk * S::QB + 4096 + (gw * 16 + (lane >> 2)) * 2;
             float sl[128 / S::GG], sh[128 / S::GG];
 #pragma unroll
             for (int q = 0; q < 128 / S::GG; ++q) {
@@ -718,51 +748,38 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
                 sh[q] = lds_bf16(sa + q * 128 + 16);
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (nt * 8 >= s.n) break;
-                uint32_t b[PL][2][4];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int pl = 0; pl < PL; ++pl) {
-                    ldmatrix4(st + xrow[nt][pl], b[pl][0]);
-                    ldmatrix4(st + xrow[nt][pl] + 64, b[pl][1]);
-                }
+                for (int t = 0; t < TILES; ++t) {
+                    if (TILES > 1 && !tile_used(t, s.n - 8 * nt)) break;
+                    uint32_t b[2][4];
+                    ldmatrix4(st + xrow[nt][t] + kb * 128, b[0]);
+                    ldmatrix4(st + xrow[nt][t] + kb * 128 + 64, b[1]);
 #pragma unroll
-                for (int q = 0; q < 128 / S::GG; ++q) {
-                    int g[PL][4];
+                    for (int q = 0; q < 128 / S::GG; ++q) {
+                        int g[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int pl = 0; pl < PL; ++pl)
-                        g[pl][0] = g[pl][1] = g[pl][2] = g[pl][3] = 0;
-#pragma unroll
-                    for (int u = q * (S::GG / 32); u < (q + 1) * (S::GG / 32); ++u)
-#pragma unroll
-                        for (int pl = 0; pl < PL; ++pl)
-                            imma_codes(g[pl], w[2 * u], w[2 * u + 1], b[pl][u / 2][2 * (u & 1)],
-                                       b[pl][u / 2][2 * (u & 1) + 1]);
-#pragma unroll
-                    for (int pl = 0; pl < PL; ++pl) {
-                        acc[nt][pl][0] = fmaf(small_int(g[pl][0]), sl[q], acc[nt][pl][0]);
-                        acc[nt][pl][1] = fmaf(small_int(g[pl][1]), sl[q], acc[nt][pl][1]);
-                        acc[nt][pl][2] = fmaf(small_int(g[pl][2]), sh[q], acc[nt][pl][2]);
-                        acc[nt][pl][3] = fmaf(small_int(g[pl][3]), sh[q], acc[nt][pl][3]);
+                        for (int u = q * (S::GG / 32); u < (q + 1) * (S::GG / 32); ++u)
+                            imma_codes(g, w[2 * u], w[2 * u + 1], b[u / 2][2 * (u & 1)],
+                                       b[u / 2][2 * (u & 1) + 1]);
+                        acc[nt][t][0] = fmaf(small_int(g[0]), sl[q], acc[nt][t][0]);
+                        acc[nt][t][1] = fmaf(small_int(g[1]), sl[q], acc[nt][t][1]);
+                        acc[nt][t][2] = fmaf(small_int(g[2]), sh[q], acc[nt][t][2]);
+                        acc[nt][t][3] = fmaf(small_int(g[3]), sh[q], acc[nt][t][3]);
                     }
                 }
-            }
         }
         c.done();
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        if (!PACKED) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                acc[nt][0][q] = fmaf(acc[nt][PL - 1][q], 65536.f,
-                                     fmaf(acc[nt][PL / 2][q], 256.f, acc[nt][0][q]));
-        }
+        float y[4];
+        join_planes<TILES>(acc[nt], y);
         float* q = red + nt * 160 + 2 * (lane & 3) * 20 + (lane >> 2);
-        q[0] = acc[nt][0][0];
-        q[20] = acc[nt][0][1];
-        q[8] = acc[nt][0][2];
-        q[28] = acc[nt][0][3];
+        q[0] = y[0];
+        q[20] = y[1];
+        q[8] = y[2];
+        q[28] = y[3];
     }
 }
 
@@ -831,93 +848,73 @@ __device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool
 }
 
 // The same for 4 bits.  hf: what the planes of H are multiplied by, per token.
-template <int G, int TT, bool PACKED>
+template <int G, int TT, int TILES>
 __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool mine, uint32_t hs,
                                         const float* hf, float* out) {
     using S = Shape<G, TT>;
-    constexpr int NT = PACKED ? 1 : S::NT, PL = PACKED ? 1 : 3;
+    constexpr int NT = TILES == 1 ? 1 : S::NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
     const int lm = lane & 7, lq = lane >> 3, ft = lane & 3;
-    uint32_t hrow[NT][PL];
-    float acc[NT][PL][4];
+    uint32_t hrow[NT][TILES];
+    float acc[NT][TILES][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int pl = 0; pl < PL; ++pl) {
-            const int col = min(lm, 3 * s.n - 1);  // packed: (token, plane)
-            const int n = PACKED ? col / 3 : min(nt * 8 + lm, s.n - 1);
-            hrow[nt][pl] = hs + n * S::HPITCH + (PACKED ? col % 3 : pl) * S::HPLANE + s.hb + lq * 16;
+        for (int t = 0; t < TILES; ++t) {
+            const int row = min(nt * 24 + t * 8 + lm, 3 * s.n - 1);
+            hrow[nt][t] = hs + row / 3 * S::HPITCH + row % 3 * S::HPLANE + s.hb + lq * 16;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[nt][pl][q] = 0.f;
+            for (int q = 0; q < 4; ++q) acc[nt][t][q] = 0.f;
         }
     for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
         const int np = min(S::PANELS, s.len / 32 - p0);
         const uint8_t* stp = c.wait();
         if (!c.lost && mine) {
-            const int first = s.j0 / 32 + p0, q0 = first * 32 / S::GG;
+            constexpr int PG = S::GG / 32;  // panels of a group
+            const int first = s.j0 / 32 + p0, q0 = first / PG;
             const uint2* cw = reinterpret_cast<const uint2*>(stp + rb * S::ROWBLK + tile * 256) + lane;
             const uint32_t sa = smem_addr(stp) + S::SCALES + rb * S::GROUPS * 256 +
                                 (tile * 16 + (lane >> 2)) * 2;
+            // the panels of one group at a time: their sum is exact
+            for (int p = 0; p < np;) {
+                const int gq = (first + p) / PG - q0;
+                const int pe = min(np, (q0 + gq + 1) * PG - first);
+                const float sl = lds_bf16(sa + gq * 256), sh = lds_bf16(sa + gq * 256 + 16);
+                uint2 w[PG];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (nt * 8 >= s.n) break;
-                int g[PL][4];
+                for (int i = 0; i < PG; ++i) w[i] = p + i < pe ? cw[(p + i) * 256] : make_uint2(0, 0);
 #pragma unroll
-                for (int pl = 0; pl < PL; ++pl) g[pl][0] = g[pl][1] = g[pl][2] = g[pl][3] = 0;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int q = 0; q < S::PANELS; q += 2) {  // H fragments serve two panels
-                    if (q >= np) break;
-                    uint32_t b[PL][4];
+                    for (int t = 0; t < TILES; ++t) {
+                        if (TILES > 1 && !tile_used(t, s.n - 8 * nt)) break;
+                        int g[2][4];
 #pragma unroll
-                    for (int pl = 0; pl < PL; ++pl) ldmatrix4(hrow[nt][pl] + (p0 + q) * 32, b[pl]);
+                        for (int q = 0; q < 4; ++q) g[0][q] = g[1][q] = 0;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (q + half >= np) break;
-                        const uint2 w = cw[(q + half) * 256];
-#pragma unroll
-                        for (int pl = 0; pl < PL; ++pl)
-                            imma_codes(g[pl], w.x, w.y, b[pl][2 * half], b[pl][2 * half + 1]);
-                        // the group ends, or the stage
-                        const int at = first + q + half;
-                        if (S::GG == 32 || (at + 1) * 32 % S::GG == 0 || q + half == np - 1) {
-                            const uint32_t sq = sa + (at * 32 / S::GG - q0) * 256;
-                            const float sl = lds_bf16(sq), sh = lds_bf16(sq + 16);
-#pragma unroll
-                            for (int pl = 0; pl < PL; ++pl) {
-                                acc[nt][pl][0] = fmaf(small_int(g[pl][0]), sl, acc[nt][pl][0]);
-                                acc[nt][pl][1] = fmaf(small_int(g[pl][1]), sl, acc[nt][pl][1]);
-                                acc[nt][pl][2] = fmaf(small_int(g[pl][2]), sh, acc[nt][pl][2]);
-                                acc[nt][pl][3] = fmaf(small_int(g[pl][3]), sh, acc[nt][pl][3]);
-                                g[pl][0] = g[pl][1] = g[pl][2] = g[pl][3] = 0;
-                            }
+                        for (int i = 0; i < PG; i += 2) {  // an H fragment serves two panels
+                            if (i && p + i >= pe) break;
+                            uint32_t b[4];
+                            ldmatrix4(hrow[nt][t] + (p0 + p + i) * 32, b);
+                            imma_codes(g[0], w[i].x, w[i].y, b[0], b[1]);
+                            // (a panel past the group has zero codes)
+                            if (PG > 1) imma_codes(g[1], w[(i + 1) % PG].x, w[(i + 1) % PG].y, b[2], b[3]);
                         }
+                        acc[nt][t][0] = fmaf(small_int(g[0][0] + g[1][0]), sl, acc[nt][t][0]);
+                        acc[nt][t][1] = fmaf(small_int(g[0][1] + g[1][1]), sl, acc[nt][t][1]);
+                        acc[nt][t][2] = fmaf(small_int(g[0][2] + g[1][2]), sh, acc[nt][t][2]);
+                        acc[nt][t][3] = fmaf(small_int(g[0][3] + g[1][3]), sh, acc[nt][t][3]);
                     }
-                }
+                p = pe;
             }
         }
         c.done();
     }
     if (!mine) return;
-    if (PACKED) {
-        // columns 2 ft, 2 ft + 1 of (token 0: planes 0, 1, 2; token 1: planes 0, 1, 2)
-        const float w0 = ft == 1 ? 65536.f : 1.f, w1 = ft == 1 ? 1.f : 256.f;
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-            const float p = acc[0][0][2 * hi], q = acc[0][0][2 * hi + 1];
-            const float t0 = ft == 0 ? fmaf(q, w1, p) : ft == 1 ? p * w0 : 0.f;
-            const float t1 = ft == 1 ? q : ft == 2 ? fmaf(q, 65536.f, p * 256.f) : 0.f;
-            const float y0 = quad_sum(t0), y1 = quad_sum(t1);
-            if (ft == 0) out[8 * hi] = y0 * hf[0];
-            if (ft == 1 && s.n > 1) out[(int64_t)d + 8 * hi] = y1 * hf[1];
-        }
-        return;
-    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         float y[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            y[q] = fmaf(acc[nt][PL - 1][q], 65536.f, fmaf(acc[nt][PL / 2][q], 256.f, acc[nt][0][q]));
+        join_planes<TILES>(acc[nt], y);
         const int n = nt * 8 + 2 * ft;
         float* q = out + (int64_t)n * d;
         if (n < s.n) {
@@ -972,7 +969,6 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
         // ---------------------------------------------------- H
         for (int i = 0; i < nseg; ++i) {
             const Seg s = segs[i];
-            const bool packed = S::Q4 && s.n <= 2;
             const int jj = gt & 7, n = gt >> 3;  // the unit of the group's 8, and the token
             const float gate = n < s.n ? r.gate[s.item][n] : 0.f;
             const float xf = S::Q4 && n < s.n ? a.xf[r.tok[s.item][n]] : 1.f;
@@ -981,25 +977,19 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                 float* mine = base + warp * (S::NT * 160);
                 if constexpr (!S::Q4)
                     up_bf16<TT>(c, s, d, mine);
-                else if (TT <= 2 || packed)
-                    up_q4<G, TT, true>(c, s, d, mine);
+                else if (TT <= 2 || s.n <= 2)
+                    up_q4<G, TT, 1>(c, s, d, mine);
                 else
-                    up_q4<G, TT, false>(c, s, d, mine);
+                    up_q4<G, TT, 3>(c, s, d, mine);
                 named_sync(2 + gw, 128);
                 if (n < s.n) {
                     float ga = 0.f, up = 0.f;
 #pragma unroll
                     for (int w = 0; w < S::KW; ++w) {
-                        const float* q = base + (gw * 4 + w) * (S::NT * 160) + jj;
-                        if (packed) {
-                            q += 3 * n * 20;
-                            ga += fmaf(q[40], 65536.f, fmaf(q[20], 256.f, q[0]));
-                            up += fmaf(q[48], 65536.f, fmaf(q[28], 256.f, q[8]));
-                        } else {
-                            q += n * 20;  // (a tile of 8 tokens is 160 floats)
-                            ga += q[0];
-                            up += q[8];
-                        }
+                        // (a tile of 8 tokens is 160 floats)
+                        const float* q = base + (gw * 4 + w) * (S::NT * 160) + n * 20 + jj;
+                        ga += q[0];
+                        up += q[8];
                     }
                     const int at = s.hb + j + gw * 8 + jj;
                     const float hv = silu_f(ga * xf) * (up * xf) * gate;
@@ -1064,9 +1054,9 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                 if constexpr (!S::Q4)
                     down_bf16<TT>(c, s, d, mine, hs, out);
                 else if (TT <= 2 || s.n <= 2)
-                    down_q4<G, TT, true>(c, s, d, mine, hs, hf[i], out);
+                    down_q4<G, TT, 1>(c, s, d, mine, hs, hf[i], out);
                 else
-                    down_q4<G, TT, false>(c, s, d, mine, hs, hf[i], out);
+                    down_q4<G, TT, 3>(c, s, d, mine, hs, hf[i], out);
             }
         }
     }
@@ -1090,6 +1080,8 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     __shared__ Seg segs[2 + TOKEN_WARPS][MAX_SEGS];
     __shared__ float hf[MAX_SEGS][FT];
     const int tid = threadIdx.x, warp = tid >> 5;
+    for (int e = tid; e < MAX_E; e += FFN_THREADS) r.tokens[e] = 0;
+    if (tid < MAX_E / 32) r.hit[tid] = 0;
     if (tid == 0) {
         for (int i = 0; i < stages; ++i) {
             // the weights' announcement and the token warps' lanes
@@ -1104,6 +1096,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         }
     }
     pdl_trigger();
+    __syncthreads();
     pdl_wait();  // the router's logits (and planes)
     route_batch(a, r);
     if (warp < CONSUMERS / 32) {
@@ -1136,46 +1129,47 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
 // ---------------------------------------------------------------- combine
 
 // out[t][c] = sum over the uses of token t (choices in order, then the shared
-// expert) and their parts of the partial rows.  A block takes 64 columns of one
-// token: 16 groups of 16 lanes share the rows, so that a row's 256 bytes are
-// one access and many rows are in flight.
-constexpr int CB_COLS = 64;
+// expert) and their parts of the partial rows.  A block takes 32 columns of one
+// token: 32 groups of 8 lanes share the rows, so that most of them are in flight at
+// once (a token of a small batch has as many rows as there are parts).
+constexpr int CB_COLS = 32;
 
 __global__ void __launch_bounds__(256) few_combine_kernel(const __grid_constant__ FewArgs a) {
-    __shared__ float4 sums[16][16];
-    const int tid = threadIdx.x, col = tid & 15, grp = tid >> 4;
+    __shared__ float4 sums[32][9];
+    const int tid = threadIdx.x, col = tid & 7, grp = tid >> 3;
     const int t = blockIdx.y, c = blockIdx.x * CB_COLS + col * 4;
     pdl_wait();
+    int4 use[MAX_K + 1];
+#pragma unroll
+    for (int j = 0; j <= MAX_K; ++j)
+        use[j] = j < a.k + (a.hsum > 0) ? a.table[t * (a.k + 1) + j] : make_int4(0, 0, 0, 0);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int uses = a.k + (a.hsum > 0);
-    for (int j = 0; j < uses; ++j) {
-        const int4 u = a.table[t * (a.k + 1) + j];
+    int at = grp;  // this group's place among the rows of the use
+#pragma unroll
+    for (int j = 0; j <= MAX_K; ++j) {
 #pragma unroll 4
-        for (int q = grp; q < u.y; q += 16) {
-            const float4 v =
-                *reinterpret_cast<const float4*>(a.part + (int64_t)(u.x + q * u.z) * a.d + c);
+        for (; at < use[j].y; at += 32) {
+            const float4 v = *reinterpret_cast<const float4*>(
+                a.part + (int64_t)(use[j].x + at * use[j].z) * a.d + c);
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
         }
+        at -= use[j].y;
     }
     sums[grp][col] = s;
     __syncthreads();
-    if (tid < 16) {
-        float4 o = sums[0][tid];
+    if (tid < CB_COLS) {
+        const float* q = reinterpret_cast<const float*>(sums) + tid;
+        float o = 0.f;
 #pragma unroll
-        for (int g = 1; g < 16; ++g) {
-            o.x += sums[g][tid].x;
-            o.y += sums[g][tid].y;
-            o.z += sums[g][tid].z;
-            o.w += sums[g][tid].w;
-        }
-        uint2 w;
-        w.x = pack_bf16x2(o.x, o.y);
-        w.y = pack_bf16x2(o.z, o.w);
-        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)t * a.d +
-                                  blockIdx.x * CB_COLS + tid * 4) = w;
+        for (int g = 0; g < 32; ++g) o += q[g * 36];
+        const float hi = __shfl_down_sync(0xffffffffu, o, 1);
+        if ((tid & 1) == 0)
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                         (int64_t)t * a.d + blockIdx.x * CB_COLS + tid) =
+                pack_bf16x2(o, hi);
     }
 }
 
@@ -1200,32 +1194,48 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
 // multiplied by.  Rows with an infinity or NaN get zeros and the factor NaN.
 __device__ void split_planes(const FewArgs& a) {
     __shared__ uint32_t top[FT];  // bits of the largest magnitude: ordered as unsigned
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int d = a.d, len = d / RC, c0 = blockIdx.y * len;
-    const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
-    for (int t = warp; t < a.T; t += ROUTER_THREADS / 32) {
+    const int tid = threadIdx.x;
+    const int d = a.d, vecs = d / RC / 8, v0 = blockIdx.y * vecs;  // 8 elements at a time
+    const uint4* x = reinterpret_cast<const uint4*>(a.x);
+    if (tid < FT) top[tid] = 0;
+    __syncthreads();
+    for (int t = 0; t < a.T; ++t) {
         uint32_t m = 0;
-        for (int c = lane; c < len; c += 32) m = max(m, x[(int64_t)t * d + c0 + c] & 0x7FFFu);
+        for (int c = tid; c < vecs; c += ROUTER_THREADS) {
+            const uint4 v = x[(int64_t)t * (d / 8) + v0 + c];
+            const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu,
+                                   v.w & 0x7FFF7FFFu};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = max(m, max(w[q] & 0xFFFFu, w[q] >> 16));
+        }
         m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) top[t] = m;
+        if ((tid & 31) == 0 && m) atomicMax(&top[t], m);
     }
     cluster_sync_all();
-    for (int t = warp; t < a.T; t += ROUTER_THREADS / 32) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < RC; ++q) m = max(m, ld_cluster_u32(map_shared_rank(smem_addr(&top[t]), q)));
+    for (int t = 0; t < a.T; ++t) {
+        if ((tid & ~31) >= vecs && tid >= 32) break;  // no work for this warp
+        uint32_t m = (tid & 31) < RC ? ld_cluster_u32(map_shared_rank(smem_addr(&top[t]), tid & 31)) : 0u;
+        m = __reduce_max_sync(0xffffffffu, m);
         const bool odd = m >= 0x7F80u;
         const int e = odd ? 0 : plane_exponent(__uint_as_float(m << 16));
-        int8_t* dst = a.xq + (int64_t)t * 3 * d + c0;
-        for (int c = lane; c < len; c += 32) {
-            const float v = __uint_as_float((uint32_t)x[(int64_t)t * d + c0 + c] << 16);
-            int8_t p[3];
-            digits(odd ? 0.f : scalbnf(v, e), p);
+        for (int c = tid; c < vecs; c += ROUTER_THREADS) {
+            const uint4 v = x[(int64_t)t * (d / 8) + v0 + c];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint64_t plane[3] = {0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < 3; ++q) dst[(int64_t)q * d + c] = p[q];
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t bits = q & 1 ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16;
+                int8_t p[3];
+                digits(odd ? 0.f : scalbnf(__uint_as_float(bits), e), p);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) plane[i] |= (uint64_t)(uint8_t)p[i] << (8 * q);
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                *reinterpret_cast<uint64_t*>(a.xq + ((int64_t)t * 3 + i) * d + (v0 + c) * 8) = plane[i];
         }
         // the codes come as 16 q
-        if (lane == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(0.0625f, -e);
+        if (tid == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(0.0625f, -e);
     }
     cluster_sync_all();  // the maxima are read before their blocks go
 }
@@ -1354,14 +1364,14 @@ int launch_ffn_tokens(const FewMaps& m, const FewArgs& a, int smem_limit, cudaSt
 }  // namespace
 
 int64_t few_part_rows(int T, int h, int E, int k, int hsum) {
-    // A hit experts serve T k assignments at most; an item of g granules meets
-    // at most g V / tot + 2 parts
+    // A hit experts serve T k assignments at most; parts hold tot / V granules or one
+    // more, so that an item of g granules meets at most g V / tot + 2 of them
     int64_t most = 0;
-    const int64_t gE = h / FEW_GRAN, gS = hsum / FEW_GRAN;
+    const int gE = h / FEW_GRAN, gS = hsum / FEW_GRAN;
     const int hi = E < T * k ? E : T * k;
     for (int A = k; A <= hi; ++A) {
-        const int64_t tot = A * gE + gS, V = few_parts(tot, FEW_CTAS);
-        const int64_t rows = (int64_t)T * k * (gE * V / tot + 2) + (gS ? T * (gS * V / tot + 2) : 0);
+        const int tot = A * gE + gS, q = tot / few_parts(tot, FEW_CTAS);
+        const int64_t rows = (int64_t)T * k * (gE / q + 2) + (gS ? T * (gS / q + 2) : 0);
         most = rows > most ? rows : most;
     }
     return most;

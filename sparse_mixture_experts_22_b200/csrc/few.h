@@ -52,13 +52,13 @@ int launch_q4_dequantize(const void* Q13, const void* Q2, void* W13, void* W2p, 
 // ---------------------------------------------------------------- the layer
 
 // Parts the experts' hidden units are cut into: `tot` granules in item order
-// (hit experts ascending, then the shared one) over V parts, part v holding
-// [v tot / V, (v + 1) tot / V); every CTA of the grid takes the same number of
-// parts within one, and none holds more than FEW_HCAP hidden units.
-__host__ __device__ inline int few_parts(int64_t tot, int ctas) {
-    const int64_t per = (int64_t)ctas * FEW_HCAP / FEW_GRAN;
-    const int64_t V = ctas * ((tot + per - 1) / per);
-    return (int)(V < tot ? V : tot);
+// (hit experts ascending, then the shared one) over V parts of tot / V granules or
+// one more; every CTA of the grid takes the same number of parts within one, and
+// none holds more than FEW_HCAP hidden units.
+__host__ __device__ inline int few_parts(int tot, int ctas) {
+    const int per = ctas * (FEW_HCAP / FEW_GRAN);
+    const int V = ctas * ((tot + per - 1) / per);
+    return V < tot ? V : tot;
 }
 
 struct FewArgs {

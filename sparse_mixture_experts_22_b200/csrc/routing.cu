@@ -28,7 +28,6 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "plan.h"
-#include "topk.cuh"
 
 namespace moe {
 
@@ -64,6 +63,32 @@ __host__ __device__ inline size_t topk_smem_bytes(int E, int nthreads) {
     if (E <= TK_SMEM_E) b += (size_t)ROUTE_BLOCK * (E + 1) * sizeof(float);
     if (E > TK_WARP_E) b += (size_t)(nthreads / 32) * E * sizeof(float);
     return b;
+}
+
+__device__ __forceinline__ float finite_or_minus_inf(float v) { return v != v ? -INFINITY : v; }
+
+// Inserts (v, e) into a descending list of at most k entries held in
+// registers; a larger value goes first, an equal one after the entries
+// already there (experts arrive in increasing index, so the lower index keeps
+// a tie).  From the insertion point on every entry shifts down one place and
+// the old k-th falls off.
+__device__ __forceinline__ void topk_insert(float* val, int* id, int k, float v, int e) {
+    if (!(id[k - 1] < 0 || v > val[k - 1])) return;
+    float cv = v;
+    int ci = e;
+    bool ins = false;
+#pragma unroll
+    for (int q = 0; q < MAX_K; ++q) {
+        if (q < k && (ins || id[q] < 0 || cv > val[q])) {
+            const float tv = val[q];
+            const int ti = id[q];
+            val[q] = cv;
+            id[q] = ci;
+            cv = tv;
+            ci = ti;
+            ins = true;
+        }
+    }
 }
 
 // Routes part `sub` of `nsub` of the ROUTE_BLOCK tokens of block `blk` with
