@@ -1777,7 +1777,14 @@ static int few_plan_or_fail(const moe_config* cfg, FewPlan* f) {
     f->off_idx = take(T * k * 4);
     f->off_gate = take(T * k * 4);
     f->off_sums = take((2 + 3 * E) * 8);
-    f->off_part = take(P.T ? (size_t)few_part_rows((int)P.T, P.h, P.E, P.k, P.hsum) * P.d * 4 : 0);
+    // (one size for bf16 and 4-bit weights)
+    int64_t rows = 0;
+    for (int G : {0, 32})
+        if (P.T) {
+            const int64_t n = few_part_rows(G, (int)P.T, P.h, P.E, P.k, P.hsum);
+            rows = n > rows ? n : rows;
+        }
+    f->off_part = take((size_t)rows * P.d * 4);
     f->total = o;
     return MOE_OK;
 }

@@ -30,26 +30,40 @@ struct Routing {
     int32_t sel[FT * MAX_K];        // [t * k + j] expert
     float g[FT * MAX_K];            // its gate
     int32_t items;                  // hit experts + the shared one
-    int32_t tot;                    // granules of all items
+    int32_t W;                      // their granules, weighted
     int32_t V;                      // parts
     int32_t expert[FEW_MAX_ITEMS];  // expert of an item, -1: shared
     int32_t n[FEW_MAX_ITEMS];       // tokens it serves
+    int32_t cost[FEW_MAX_ITEMS];    // weight of a granule
+    int32_t at[FEW_MAX_ITEMS];      // weighted granules before it
     int32_t row0[FEW_MAX_ITEMS];    // first row of its partial outputs
     uint8_t tok[FEW_MAX_ITEMS][FT];
     float gate[FEW_MAX_ITEMS][FT];
 };
 
-// First granule of part v, and the part that holds granule x: the first tot % V
-// parts hold one granule more than the others.
-__device__ __forceinline__ int part_start(int v, int tot, int V) {
-    return v * (tot / V) + min(v, tot % V);
-}
-__device__ __forceinline__ int part_of(int x, int tot, int V) {
-    const int q = tot / V, more = tot % V;
+// Where part v begins, and the part that holds x, on the scale of granules weighted
+// by their items' costs: the first W % V parts are one longer than the others.
+__device__ __forceinline__ int part_start(int v, int W, int V) { return v * (W / V) + min(v, W % V); }
+__device__ __forceinline__ int part_of(int x, int W, int V) {
+    const int q = W / V, more = W % V;
     return x < more * (q + 1) ? x / (q + 1) : more + (x - more * (q + 1)) / q;
 }
 
-__device__ __forceinline__ int item_start(int i, int A, int gE) { return min(i, A) * gE; }
+// First and last part of an item of g granules.
+__device__ __forceinline__ int first_part(const Routing& r, int i) { return part_of(r.at[i], r.W, r.V); }
+__device__ __forceinline__ int last_part(const Routing& r, int i, int g) {
+    return part_of(r.at[i] + (g - 1) * r.cost[i], r.W, r.V);
+}
+
+// Sum over this lane and the ones below.
+__device__ __forceinline__ int warp_prefix(int v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if ((threadIdx.x & 31) >= o) v += u;
+    }
+    return v;
+}
 
 // Number of hit experts below e.
 __device__ __forceinline__ int hits_below(const Routing& r, int e) {
@@ -134,8 +148,7 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
     }
     __syncthreads();
     const int A = hits_below(r, a.E - 1) + (r.tokens[a.E - 1] != 0);
-    const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
-    const int tot = A * gE + gS, V = few_parts(tot, gridDim.x);
+    const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN, items = A + (gS > 0);
     if (tid < N) {
         const int e = r.sel[tid], t = tid / k, at = hits_below(r, e);
         const uint32_t who = r.tokens[e];
@@ -158,28 +171,36 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
             r.expert[A] = -1;
             r.n[A] = a.T;
         }
-        r.items = A + (gS > 0);
-        r.tot = tot;
-        r.V = V;
+        r.items = items;
     }
     __syncthreads();
-    // exclusive prefix over the items of tokens x parts
+    // two prefixes over the items: weighted granules, then tokens x parts
     if (tid < 32) {
-        int before = 0;
-        for (int i0 = 0; i0 < r.items; i0 += 32) {
+        int before = 0, heaviest = 0;
+        for (int i0 = 0; i0 < items; i0 += 32) {
             const int i = i0 + tid;
-            int rows = 0;
-            if (i < r.items) {
-                const int s = item_start(i, A, gE), e = s + (i < A ? gE : gS);
-                rows = r.n[i] * (part_of(e - 1, tot, V) - part_of(s, tot, V) + 1);
+            const int cost = i < items ? few_cost(a.G, r.n[i]) : 0;
+            const int w = cost * (i < A ? gE : gS);
+            const int incl = warp_prefix(w);
+            if (i < items) {
+                r.cost[i] = cost;
+                r.at[i] = before + incl - w;
             }
-            int incl = rows;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (tid >= o) incl += v;
-            }
-            if (i < r.items) r.row0[i] = before + incl - rows;
+            before += __shfl_sync(0xffffffffu, incl, 31);
+            heaviest = max(heaviest, (int)__reduce_max_sync(0xffffffffu, (unsigned)cost));
+        }
+        if (tid == 0) {
+            r.W = before;
+            r.V = few_parts(before, heaviest, gridDim.x);
+        }
+        __syncwarp();
+        before = 0;
+        for (int i0 = 0; i0 < items; i0 += 32) {
+            const int i = i0 + tid;
+            const int rows =
+                i < items ? r.n[i] * (last_part(r, i, i < A ? gE : gS) - first_part(r, i) + 1) : 0;
+            const int incl = warp_prefix(rows);
+            if (i < items) r.row0[i] = before + incl - rows;
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
@@ -204,9 +225,8 @@ __device__ void publish_routing(const FewArgs& a, const Routing& r) {
         const int pos = shared ? t : __popc(r.tokens[r.sel[i]] & ((1u << t) - 1));
         int4 row = make_int4(0, 0, 0, 0);
         if (shared ? gS > 0 : pos < a.C) {
-            const int s = item_start(item, A, gE), e = s + (shared ? gS : gE);
             row.x = r.row0[item] + pos;
-            row.y = part_of(e - 1, r.tot, r.V) - part_of(s, r.tot, r.V) + 1;
+            row.y = last_part(r, item, shared ? gS : gE) - first_part(r, item) + 1;
             row.z = r.n[item];
         }
         a.table[t * (k + 1) + (shared ? k : i % k)] = row;
@@ -278,20 +298,22 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 }
 
 // c (16 x 8, int32) += a (16 x 32) b (32 x 8), signed 8-bit
-__device__ __forceinline__ void imma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                     uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void imma(int (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                     uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
         " {%8, %9}, {%0, %1, %2, %3};"
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// c += 16 q by b for the 32 columns of two code words.
-__device__ __forceinline__ void imma_codes(int (&c)[4], uint32_t w0, uint32_t w1, uint32_t b0,
-                                           uint32_t b1) {
+// Two code words (32 columns) as an A fragment of values 16 q.
+__device__ __forceinline__ void codes_to_frag(uint32_t w0, uint32_t w1, uint32_t (&f)[4]) {
     constexpr uint32_t M = 0xF0F0F0F0u;
-    imma(c, w0 & M, (w0 << 4) & M, w1 & M, (w1 << 4) & M, b0, b1);
+    f[0] = w0 & M;
+    f[1] = (w0 << 4) & M;
+    f[2] = w1 & M;
+    f[3] = (w1 << 4) & M;
 }
 
 // An integer of magnitude below 2^22 to fp32 (an addition instead of the slower
@@ -361,8 +383,9 @@ struct Shape {
     // H: bf16 high then low parts [2][NT * 8][HPITCH]; 4 bits [TT][HPITCH], a row
     // first fp32, then its three planes HPLANE bytes apart (33 and 131 times 16 bytes:
     // rows of consecutive (token, plane) meet no bank twice)
-    [[maybe_unused]] static constexpr int HPLANE = FEW_HCAP + 16;
+    static constexpr int HPLANE = FEW_HCAP + 16;
     static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 48 : (FEW_HCAP + 8) * 2;
+    static_assert(!Q4 || 3 * HPLANE <= HPITCH, "the planes fit the row they replace");
     static constexpr int HPART = NT * 8 * HPITCH;
     static constexpr int HBYTES = Q4 ? TT * HPITCH : 2 * HPART;
     static constexpr int RED = 2 * 16 * NT * 640;          // the warps' sums, two granules
@@ -388,36 +411,50 @@ struct Seg {
     int j0, len;           // hidden units j0 .. j0 + len
     int row;               // its first row of the partial outputs
     int hb;                // where its H begins
+
+    // Panels of 32 units a stage of the second half takes: as few stages of at most
+    // `most` as there can be, of even size.
+    __device__ __forceinline__ int step(int most) const {
+        const int panels = len / 32, stages = (panels + most - 1) / most;
+        return (panels + stages - 1) / stages;
+    }
 };
 
-// Share i of part v; false past the last one.
-__device__ __forceinline__ bool segment(const FewArgs& a, const Routing& r, int v, int i, Seg& s) {
-    const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
-    const int A = r.items - (gS > 0);
-    const int g0 = part_start(v, r.tot, r.V), g1 = part_start(v + 1, r.tot, r.V);
-    s.item = min(g0 / gE, A) + i;
-    if (s.item >= r.items) return false;
-    const int is = item_start(s.item, A, gE);
-    const int s0 = max(is, g0), s1 = min(is + (s.item < A ? gE : gS), g1);
-    if (s0 >= s1) return false;
-    s.expert = r.expert[s.item];
-    s.n = r.n[s.item];
-    s.j0 = (s0 - is) * FEW_GRAN;
-    s.len = (s1 - s0) * FEW_GRAN;
-    s.row = r.row0[s.item] + (v - part_of(is, r.tot, r.V)) * s.n;
-    s.hb = (s0 - g0) * FEW_GRAN;
-    return true;
-}
-
-// A warp writes part v's shares to segs; returns how many there are.
+// A warp writes part v's shares to segs; returns how many there are.  A granule
+// belongs to the part in which it begins.
 __device__ __forceinline__ int segments(const FewArgs& a, const Routing& r, int v, Seg* segs) {
     const int lane = threadIdx.x & 31;
-    Seg s;
-    const bool have = lane < MAX_SEGS && segment(a, r, v, lane, s);
+    const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
+    const int A = r.items - (gS > 0);
+    const int w0 = part_start(v, r.W, r.V), w1 = part_start(v + 1, r.W, r.V);
+    int first = -1;  // the last item that begins at or before w0
+    for (int i0 = 0; i0 < r.items; i0 += 32)
+        first += __popc(__ballot_sync(0xffffffffu, i0 + lane < r.items && r.at[i0 + lane] <= w0));
+    const int i = first + lane;
+    int s0 = 0, s1 = 0;
+    if (lane <= MAX_SEGS && i < r.items) {
+        const int at = r.at[i], cost = r.cost[i], g = i < A ? gE : gS;
+        s0 = max(0, (w0 - at + cost - 1) / cost);
+        s1 = min(g, max(0, (w1 - at + cost - 1) / cost));
+    }
+    const bool have = s0 < s1;
+    const int len = have ? (s1 - s0) * FEW_GRAN : 0;
+    const int hb = warp_prefix(len) - len;
+    const uint32_t all = __ballot_sync(0xffffffffu, have);
     __syncwarp();
-    if (have) segs[lane] = s;
+    if (have) {
+        Seg s;
+        s.item = i;
+        s.expert = r.expert[i];
+        s.n = r.n[i];
+        s.j0 = s0 * FEW_GRAN;
+        s.len = len;
+        s.row = r.row0[i] + (v - first_part(r, i)) * s.n;
+        s.hb = hb;
+        segs[__popc(all & ((1u << lane) - 1))] = s;
+    }
     __syncwarp();
-    return __popc(__ballot_sync(0xffffffffu, have));
+    return __popc(all);
 }
 
 // A ring position: stage and the parity of its current phase.
@@ -512,15 +549,15 @@ __device__ __forceinline__ bool bring_weights(const FewArgs& a, const Routing& r
             const CUtensorMap* map = shared ? &maps.w2s : &maps.w2;
             // this lane's copy of a stage: block of rows and, for 4 bits, codes (0) or
             // scales (1), else the panel
-            const int b = lane & 1, what = lane >> 1;
+            const int b = lane & 1, what = lane >> 1, step = s.step(S::PANELS);
             const uint8_t* codes = reinterpret_cast<const uint8_t*>(shared ? a.w2s : a.w2);
             const uint8_t* scales = codes + q2_code_bytes(shared ? 1 : a.E, hid, d);
             codes += ((int64_t)e * (d / 128) + b) * (hid / 32) * 2048;
             scales += ((int64_t)e * (d / 128) + b) * (hid / S::GG) * 256;
             for (int r0 = 0; r0 < d; r0 += 256) {
                 const int nb = min(2, (d - r0) / 128);
-                for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
-                    const int np = min(S::PANELS, s.len / 32 - p0);
+                for (int p0 = 0; p0 < s.len / 32; p0 += step) {
+                    const int np = min(step, s.len / 32 - p0);
                     const int pp = s.j0 / 32 + p0;
                     if (!c.open()) return false;
                     if (S::Q4) {
@@ -583,7 +620,8 @@ __device__ __forceinline__ bool bring_tokens(const FewArgs& a, const Routing& r,
                 }
         }
         for (int i = 0; i < nseg; ++i) {
-            const int stages = (a.d + 255) / 256 * ((segs[i].len / 32 + S::PANELS - 1) / S::PANELS);
+            const int step = segs[i].step(S::PANELS);
+            const int stages = (a.d + 255) / 256 * ((segs[i].len / 32 + step - 1) / step);
             for (int q = 0; q < stages; ++q) {
                 if (!c.open()) return false;
                 mbar_arrive(c.bar());
@@ -737,9 +775,14 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
             if (c.lost || k0 + kw * S::KP + kb * 128 >= d) break;
             const int blk = kw * (S::KP / 128) + kb;
             const uint4* cw = reinterpret_cast<const uint4*>(stp + blk * S::QB + gw * 1024);
-            uint32_t w[8];
-            *reinterpret_cast<uint4*>(w) = cw[lane];
-            *reinterpret_cast<uint4*>(w + 4) = cw[32 + lane];
+            uint32_t f[4][4];
+            {
+                const uint4 lo = cw[lane], hi = cw[32 + lane];
+                codes_to_frag(lo.x, lo.y, f[0]);
+                codes_to_frag(lo.z, lo.w, f[1]);
+                codes_to_frag(hi.x, hi.y, f[2]);
+                codes_to_frag(hi.z, hi.w, f[3]);
+            }
             const uint32_t sa = st + blk * S::QB + 4096 + (gw * 16 + (lane >> 2)) * 2;
             float sl[128 / S::GG], sh[128 / S::GG];
 #pragma unroll
@@ -760,8 +803,7 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
                         int g[4] = {0, 0, 0, 0};
 #pragma unroll
                         for (int u = q * (S::GG / 32); u < (q + 1) * (S::GG / 32); ++u)
-                            imma_codes(g, w[2 * u], w[2 * u + 1], b[u / 2][2 * (u & 1)],
-                                       b[u / 2][2 * (u & 1) + 1]);
+                            imma(g, f[u], b[u / 2][2 * (u & 1)], b[u / 2][2 * (u & 1) + 1]);
                         acc[nt][t][0] = fmaf(small_int(g[0]), sl[q], acc[nt][t][0]);
                         acc[nt][t][1] = fmaf(small_int(g[1]), sl[q], acc[nt][t][1]);
                         acc[nt][t][2] = fmaf(small_int(g[2]), sh[q], acc[nt][t][2]);
@@ -803,8 +845,9 @@ __device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[nt][q] = low[nt][q] = 0.f;
     }
-    for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
-        const int np = min(S::PANELS, s.len / 32 - p0);
+    const int step = s.step(S::PANELS);
+    for (int p0 = 0; p0 < s.len / 32; p0 += step) {
+        const int np = min(step, s.len / 32 - p0);
         const uint32_t st = smem_addr(c.wait());
         if (!c.lost && mine) {
 #pragma unroll
@@ -866,8 +909,9 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
 #pragma unroll
             for (int q = 0; q < 4; ++q) acc[nt][t][q] = 0.f;
         }
-    for (int p0 = 0; p0 < s.len / 32; p0 += S::PANELS) {
-        const int np = min(S::PANELS, s.len / 32 - p0);
+    const int step = s.step(S::PANELS);
+    for (int p0 = 0; p0 < s.len / 32; p0 += step) {
+        const int np = min(step, s.len / 32 - p0);
         const uint8_t* stp = c.wait();
         if (!c.lost && mine) {
             constexpr int PG = S::GG / 32;  // panels of a group
@@ -880,9 +924,12 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
                 const int gq = (first + p) / PG - q0;
                 const int pe = min(np, (q0 + gq + 1) * PG - first);
                 const float sl = lds_bf16(sa + gq * 256), sh = lds_bf16(sa + gq * 256 + 16);
-                uint2 w[PG];
+                uint32_t f[PG][4];
 #pragma unroll
-                for (int i = 0; i < PG; ++i) w[i] = p + i < pe ? cw[(p + i) * 256] : make_uint2(0, 0);
+                for (int i = 0; i < PG; ++i) {
+                    const uint2 w = p + i < pe ? cw[(p + i) * 256] : make_uint2(0, 0);
+                    codes_to_frag(w.x, w.y, f[i]);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -896,9 +943,9 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
                             if (i && p + i >= pe) break;
                             uint32_t b[4];
                             ldmatrix4(hrow[nt][t] + (p0 + p + i) * 32, b);
-                            imma_codes(g[0], w[i].x, w[i].y, b[0], b[1]);
+                            imma(g[0], f[i], b[0], b[1]);
                             // (a panel past the group has zero codes)
-                            if (PG > 1) imma_codes(g[1], w[(i + 1) % PG].x, w[(i + 1) % PG].y, b[2], b[3]);
+                            if (PG > 1) imma(g[1], f[(i + 1) % PG], b[2], b[3]);
                         }
                         acc[nt][t][0] = fmaf(small_int(g[0][0] + g[1][0]), sl, acc[nt][t][0]);
                         acc[nt][t][1] = fmaf(small_int(g[0][1] + g[1][1]), sl, acc[nt][t][1]);
@@ -1197,11 +1244,11 @@ __device__ void split_planes(const FewArgs& a) {
     const int tid = threadIdx.x;
     const int d = a.d, vecs = d / RC / 8, v0 = blockIdx.y * vecs;  // 8 elements at a time
     const uint4* x = reinterpret_cast<const uint4*>(a.x);
-    if (tid < FT) top[tid] = 0;
-    __syncthreads();
-    for (int t = 0; t < a.T; ++t) {
+    const int lane = tid & 31, warp = tid >> 5;
+    for (int t = warp; t < a.T; t += ROUTER_THREADS / 32) {
         uint32_t m = 0;
-        for (int c = tid; c < vecs; c += ROUTER_THREADS) {
+#pragma unroll 4
+        for (int c = lane; c < vecs; c += 32) {
             const uint4 v = x[(int64_t)t * (d / 8) + v0 + c];
             const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu,
                                    v.w & 0x7FFF7FFFu};
@@ -1209,16 +1256,16 @@ __device__ void split_planes(const FewArgs& a) {
             for (int q = 0; q < 4; ++q) m = max(m, max(w[q] & 0xFFFFu, w[q] >> 16));
         }
         m = __reduce_max_sync(0xffffffffu, m);
-        if ((tid & 31) == 0 && m) atomicMax(&top[t], m);
+        if (lane == 0) top[t] = m;
     }
     cluster_sync_all();
-    for (int t = 0; t < a.T; ++t) {
-        if ((tid & ~31) >= vecs && tid >= 32) break;  // no work for this warp
-        uint32_t m = (tid & 31) < RC ? ld_cluster_u32(map_shared_rank(smem_addr(&top[t]), tid & 31)) : 0u;
+    for (int t = warp; t < a.T; t += ROUTER_THREADS / 32) {
+        uint32_t m = lane < RC ? ld_cluster_u32(map_shared_rank(smem_addr(&top[t]), lane)) : 0u;
         m = __reduce_max_sync(0xffffffffu, m);
         const bool odd = m >= 0x7F80u;
         const int e = odd ? 0 : plane_exponent(__uint_as_float(m << 16));
-        for (int c = tid; c < vecs; c += ROUTER_THREADS) {
+#pragma unroll 2
+        for (int c = lane; c < vecs; c += 32) {
             const uint4 v = x[(int64_t)t * (d / 8) + v0 + c];
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint64_t plane[3] = {0, 0, 0};
@@ -1235,7 +1282,7 @@ __device__ void split_planes(const FewArgs& a) {
                 *reinterpret_cast<uint64_t*>(a.xq + ((int64_t)t * 3 + i) * d + (v0 + c) * 8) = plane[i];
         }
         // the codes come as 16 q
-        if (tid == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(0.0625f, -e);
+        if (lane == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(0.0625f, -e);
     }
     cluster_sync_all();  // the maxima are read before their blocks go
 }
@@ -1363,18 +1410,24 @@ int launch_ffn_tokens(const FewMaps& m, const FewArgs& a, int smem_limit, cudaSt
 
 }  // namespace
 
-int64_t few_part_rows(int T, int h, int E, int k, int hsum) {
-    // A hit experts serve T k assignments at most; parts hold tot / V granules or one
-    // more, so that an item of g granules meets at most g V / tot + 2 of them
-    int64_t most = 0;
-    const int gE = h / FEW_GRAN, gS = hsum / FEW_GRAN;
-    const int hi = E < T * k ? E : T * k;
-    for (int A = k; A <= hi; ++A) {
-        const int tot = A * gE + gS, q = tot / few_parts(tot, FEW_CTAS);
-        const int64_t rows = (int64_t)T * k * (gE / q + 2) + (gS ? T * (gS / q + 2) : 0);
-        most = rows > most ? rows : most;
+int64_t few_part_rows(int G, int T, int h, int E, int k, int hsum) {
+    // Parts are at least W / V long rounded down, and no shorter than the costliest
+    // granule, so an item of weight w meets at most w V / W + 2 of them; n tokens
+    // then take n w V / W + 2 n rows.  The sum over the items of n w is at most T W,
+    // and at most (greatest cost / least cost) times what equal costs would make it.
+    const int least = few_cost(G, 1), most = few_cost(G, T);
+    const int64_t gE = h / FEW_GRAN, gS = hsum / FEW_GRAN, N = (int64_t)T * k;
+    int64_t rows = 0;
+    for (int64_t A = k; A <= (E < N ? E : N); ++A) {
+        const int64_t tot = A * gE + gS;
+        const int64_t V = few_parts((int)(tot * most), least, FEW_CTAS);
+        const int64_t even = (N * gE + T * gS) * V / tot + 1;  // sum of n w V / W at equal costs
+        const int64_t skewed = even * most / least + 1, all = T * V;
+        // (rounding W / V down lengthens w V / W by less than one part in 15)
+        const int64_t need = (skewed < all ? skewed : all) * 16 / 15 + 2 * (N + T);
+        rows = need > rows ? need : rows;
     }
-    return most;
+    return rows;
 }
 
 int launch_few_router(const FewArgs& a, const float* Wr, float* z, cudaStream_t st) {

@@ -51,14 +51,22 @@ int launch_q4_dequantize(const void* Q13, const void* Q2, void* W13, void* W2p, 
 
 // ---------------------------------------------------------------- the layer
 
-// Parts the experts' hidden units are cut into: `tot` granules in item order
-// (hit experts ascending, then the shared one) over V parts of tot / V granules or
-// one more; every CTA of the grid takes the same number of parts within one, and
-// none holds more than FEW_HCAP hidden units.
-__host__ __device__ inline int few_parts(int tot, int ctas) {
-    const int per = ctas * (FEW_HCAP / FEW_GRAN);
-    const int V = ctas * ((tot + per - 1) / per);
-    return V < tot ? V : tot;
+// What a granule costs an SM when its expert serves n tokens, in eighths of
+// bringing it in: where products take longer than HBM, a part holds fewer granules.
+__host__ __device__ inline int few_cost(int G, int n) {
+    if (G == 0 || n <= 2) return 8;
+    return n <= 5 ? 9 : n <= 8 ? 12 : 20;
+}
+
+// Parts the experts' hidden units are cut into: W weighted granules in item order
+// (hit experts ascending, then the shared one) over V parts of W / V or one more;
+// every CTA of the grid takes the same number of parts within one, none holds more
+// than FEW_HCAP hidden units (a granule costs 8 at least, and one may begin at the
+// very end), and none is shorter than the costliest granule.
+__host__ __device__ inline int few_parts(int W, int heaviest, int ctas) {
+    const int per = ctas * (FEW_HCAP / FEW_GRAN - 1) * 8;
+    const int V = ctas * ((W + per - 1) / per), most = W / heaviest;
+    return V < most ? V : most;
 }
 
 struct FewArgs {
@@ -88,7 +96,7 @@ struct FewArgs {
 };
 
 // Upper bound on the rows of FewArgs::part for any routing of the batch.
-int64_t few_part_rows(int T, int h, int E, int k, int hsum);
+int64_t few_part_rows(int G, int T, int h, int E, int k, int hsum);
 // Logits z [T][E] = x Wr; clears the status word; with 4-bit weights (a.G) also
 // splits x into its planes.
 int launch_few_router(const FewArgs& a, const float* Wr, float* z, cudaStream_t st);
