@@ -30,6 +30,7 @@ struct Routing {
     int32_t sel[FT * MAX_K];        // [t * k + j] expert
     float g[FT * MAX_K];            // its gate
     int32_t items;                  // hit experts + the shared one
+    int32_t most;                   // tokens of the one that serves most
     int32_t W;                      // their granules, weighted
     int32_t V;                      // parts
     int32_t expert[FEW_MAX_ITEMS];  // expert of an item, -1: shared
@@ -176,7 +177,7 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
     __syncthreads();
     // two prefixes over the items: weighted granules, then tokens x parts
     if (tid < 32) {
-        int before = 0, heaviest = 0;
+        int before = 0, heaviest = 0, most = 0;
         for (int i0 = 0; i0 < items; i0 += 32) {
             const int i = i0 + tid;
             const int cost = i < items ? few_cost(a.G, r.n[i]) : 0;
@@ -188,8 +189,10 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
             heaviest = max(heaviest, (int)__reduce_max_sync(0xffffffffu, (unsigned)cost));
+            most = max(most, (int)__reduce_max_sync(0xffffffffu, i < items ? (unsigned)r.n[i] : 0u));
         }
         if (tid == 0) {
+            r.most = most;
             r.W = before;
             r.V = few_parts(before, heaviest, gridDim.x);
         }
@@ -365,41 +368,74 @@ template <int G, int TT>   // group (0: bf16), most tokens
 struct Shape {
     static constexpr bool Q4 = G > 0;
     static constexpr int GG = Q4 ? G : 128;
-    static constexpr int NT = (TT + 7) / 8;                // tiles of 8 tokens
-    static constexpr int KP = Q4 ? (TT <= 2 ? 256 : 128) : 64;  // columns of a warp in a stage
     static constexpr int KW = 4;                           // warps along the columns
-    static constexpr int KA = KW * KP;                     // columns of a stage
+    static constexpr int KB = Q4 ? 128 : 64;               // least columns of a warp in a stage
     static constexpr int QB = q13_block_bytes(GG);
     static constexpr int XROWS = Q4 ? 3 : 1;               // rows of a stage per token
     static constexpr int XBYTES = Q4 ? 1 : 2;              // bytes of an element
-    static constexpr int XPITCH = KA * XBYTES + 16;
-    static constexpr int XOFF = Q4 ? KA / 128 * QB : KA * 128;  // where the tokens begin
-    // second half: 2 blocks of 128 rows x panels of 32 units
-    static constexpr int PANELS = Q4 ? 8 : 2;
-    static constexpr int ROWBLK = Q4 ? PANELS * 2048 : 8192;    // bytes of a block of rows
-    static constexpr int SCALES = 2 * PANELS * 2048;            // 4 bits: where its scales begin
-    // groups that the panels can meet
-    static constexpr int GROUPS = GG == 32 ? PANELS : PANELS * 32 / GG + 1;
-    // H: bf16 high then low parts [2][NT * 8][HPITCH]; 4 bits [TT][HPITCH], a row
-    // first fp32, then its three planes HPLANE bytes apart (33 and 131 times 16 bytes:
-    // rows of consecutive (token, plane) meet no bank twice)
+    // a stage of the second half: 2 blocks of 128 rows x panels of 32 units, with 4
+    // bits then the scales of the groups they meet (one more than they fill, unless a
+    // group is a panel)
+    static constexpr int PANEL = Q4 ? 2048 : 8192;         // bytes of 128 rows of a panel
+    static __device__ __forceinline__ int groups(int panels) {
+        return GG == 32 ? panels : panels * 32 / GG + 1;
+    }
+    static __device__ __forceinline__ int down(int panels) {
+        return 2 * panels * PANEL + (Q4 ? 2 * groups(panels) * 256 : 0);
+    }
+    // H: bf16 high, then low parts of the tokens' rows; 4 bits: a row first fp32, then
+    // its three planes HPLANE bytes apart (33 and 131 times 16 bytes: rows of
+    // consecutive (token, plane) meet no bank twice)
     static constexpr int HPLANE = FEW_HCAP + 16;
     static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 48 : (FEW_HCAP + 8) * 2;
     static_assert(!Q4 || 3 * HPLANE <= HPITCH, "the planes fit the row they replace");
-    static constexpr int HPART = NT * 8 * HPITCH;
-    static constexpr int HBYTES = Q4 ? TT * HPITCH : 2 * HPART;
-    static constexpr int RED = 2 * 16 * NT * 640;          // the warps' sums, two granules
-    static __host__ __device__ int slot(int T) {
-        const int up = XOFF + T * XROWS * XPITCH;
-        const int down = Q4 ? SCALES + 2 * GROUPS * 256 : 32768;
-        return ((up > down ? up : down) + 1023) / 1024 * 1024;
-    }
-    static __host__ __device__ size_t fixed() {
-        return 1024 + (HBYTES + 15) / 16 * 16 + RED + sizeof(Routing) + 512;
-    }
+};
+
+// Shared memory of one call: the ring, H and the warps' sums are sized by the most
+// tokens an expert of the batch serves, not by the batch.
+struct Geometry {
+    int blocks;   // blocks of KB columns of a warp in a stage of the first half
+    int panels;   // panels of 32 hidden units in a stage of the second
+    int ka;       // columns of a stage of the first half
+    int xpitch;   // bytes of a token's row in it, and where the rows begin
+    int xoff;
+    int slot;     // bytes of a stage
+    int stages;
+    int nt;       // tiles of 8 tokens
+    int hpart;    // bytes from H's high to its low parts (bf16)
+    int h, red;   // where H and the warps' sums begin, behind the ring
 };
 
 constexpr int MAX_STAGES = 12;
+
+// 4 bits: stages of two blocks and eight panels where four of them fit, else half of
+// that: fewer stages are fewer waits (decode layer, one token: 54.6 us against 63.8),
+// but one of them is being read, and what the others hold has to cover HBM's latency.
+template <typename S>
+__device__ __forceinline__ Geometry geometry(int tokens, int bytes) {
+    Geometry g;
+    g.nt = (tokens + 7) / 8;
+    g.hpart = g.nt * 8 * S::HPITCH;
+    const int h = (S::Q4 ? tokens * S::HPITCH : 2 * g.hpart + 15) / 16 * 16;
+    const int red = 2 * 16 * g.nt * 640;   // two granules' sums of 16 warps
+    const int ring = bytes - h - red;
+#pragma unroll
+    for (int blocks = S::Q4 ? 2 : 1; blocks >= 1; --blocks) {
+        g.blocks = blocks;
+        g.panels = S::Q4 ? 4 * blocks : 2;
+        g.ka = S::KW * S::KB * blocks;
+        g.xpitch = g.ka * S::XBYTES + 16;
+        g.xoff = S::Q4 ? g.ka / 128 * S::QB : g.ka * 128;
+        const int up = g.xoff + tokens * S::XROWS * g.xpitch;
+        g.slot = (max(up, S::down(g.panels)) + 1023) / 1024 * 1024;
+        g.stages = min(ring / g.slot, MAX_STAGES);
+        if (g.stages >= 4) break;
+    }
+    g.h = g.stages * g.slot;
+    g.red = g.h + h;
+    return g;
+}
+
 constexpr int CONSUMERS = 512;
 constexpr int TOKEN_WARPS = 3;
 constexpr int FFN_THREADS = CONSUMERS + 32 + TOKEN_WARPS * 32;
@@ -474,14 +510,14 @@ struct Bringer {
     uint8_t* ring;
     uint64_t *full, *empty;
     uint64_t limit;
-    int slot;
+    Geometry geo;
     Ring p;
 
     // Waits until the stage is free; false if the wait ran out (the same in all lanes).
     __device__ __forceinline__ bool open() {
         return __all_sync(0xffffffffu, mbar_wait(&empty[p.stage], p.phase ^ 1, limit));
     }
-    __device__ __forceinline__ uint32_t at() const { return smem_addr(ring) + p.stage * slot; }
+    __device__ __forceinline__ uint32_t at() const { return smem_addr(ring) + p.stage * geo.slot; }
     __device__ __forceinline__ uint64_t* bar() const { return &full[p.stage]; }
 };
 
@@ -516,8 +552,8 @@ __device__ __forceinline__ bool bring_weights(const FewArgs& a, const Routing& r
                                  ((int64_t)e * (hid / 32) + s.j0 / 32) * (d / 128) * S::QB;
             int block = 2 * (int)(((int64_t)e * hid + s.j0) / 128), row = s.j0 % 128;
             for (int j = 0; j < s.len; j += FEW_GRAN) {
-                for (int k0 = 0; k0 < d; k0 += S::KA) {
-                    const int kn = min(S::KA, d - k0);
+                for (int k0 = 0; k0 < d; k0 += c.geo.ka) {
+                    const int kn = min(c.geo.ka, d - k0);
                     if (!c.open()) return false;
                     if (S::Q4) {
                         const uint32_t bytes = kn / 128 * S::QB;
@@ -549,9 +585,10 @@ __device__ __forceinline__ bool bring_weights(const FewArgs& a, const Routing& r
             const CUtensorMap* map = shared ? &maps.w2s : &maps.w2;
             // this lane's copy of a stage: block of rows and, for 4 bits, codes (0) or
             // scales (1), else the panel
-            const int b = lane & 1, what = lane >> 1, step = s.step(S::PANELS);
+            const int b = lane & 1, what = lane >> 1, step = s.step(c.geo.panels);
             const uint8_t* codes = reinterpret_cast<const uint8_t*>(shared ? a.w2s : a.w2);
             const uint8_t* scales = codes + q2_code_bytes(shared ? 1 : a.E, hid, d);
+            const int block = c.geo.panels * S::PANEL, scale = S::groups(c.geo.panels) * 256;
             codes += ((int64_t)e * (d / 128) + b) * (hid / 32) * 2048;
             scales += ((int64_t)e * (d / 128) + b) * (hid / S::GG) * 256;
             for (int r0 = 0; r0 < d; r0 += 256) {
@@ -564,7 +601,7 @@ __device__ __forceinline__ bool bring_weights(const FewArgs& a, const Routing& r
                         const int q0 = pp * 32 / S::GG, nq = ((pp + np) * 32 - 1) / S::GG - q0 + 1;
                         announce(nb * (np * 2048 + nq * 256));
                         if (b < nb && what < 2)
-                            bulk_load(c.at() + (what ? S::SCALES + b * S::GROUPS * 256 : b * S::ROWBLK),
+                            bulk_load(c.at() + (what ? 2 * block + b * scale : b * block),
                                       what ? scales + q0 * 256 : codes + (int64_t)pp * 2048,
                                       what ? nq * 256 : np * 2048, c.bar(), once);
                     } else {
@@ -590,7 +627,7 @@ template <int G, int TT>
 __device__ __forceinline__ bool bring_tokens(const FewArgs& a, const Routing& r, Seg* segs,
                                              Bringer c, int share) {
     using S = Shape<G, TT>;
-    constexpr int ROW = S::KA * S::XBYTES;  // bytes of a stage's row
+    const int rowbytes = c.geo.ka * S::XBYTES;  // of a stage: one copy of every lane, or two
     const int lane = threadIdx.x & 31;
     const int pitch = a.d * S::XBYTES;  // bytes of a row in memory
     const uint8_t* x = reinterpret_cast<const uint8_t*>(S::Q4 ? (const void*)a.xq : a.x) + lane * 16;
@@ -605,22 +642,23 @@ __device__ __forceinline__ bool bring_tokens(const FewArgs& a, const Routing& r,
                                               mine % S::XROWS) * pitch
                                            : 0;
             for (int j = 0; j < s.len; j += FEW_GRAN)
-                for (int k0 = 0; k0 < pitch; k0 += ROW) {
+                for (int k0 = 0; k0 < pitch; k0 += rowbytes) {
                     if (!c.open()) return false;
-                    const uint32_t dst = c.at() + S::XOFF + lane * 16;
+                    const uint32_t dst = c.at() + c.geo.xoff + lane * 16;
                     for (int q = 0, row = share; row < rows; ++q, row += TOKEN_WARPS) {
                         const int64_t from = __shfl_sync(0xffffffffu, at, q);
-#pragma unroll
-                        for (int w = 0; w < ROW; w += 512)
-                            if (k0 + w + lane * 16 < pitch)
-                                cp_async16(dst + row * S::XPITCH + w, x + from + k0 + w);
+                        const uint8_t* src = x + from + k0;
+                        const uint32_t to = dst + row * c.geo.xpitch;
+                        if (k0 + lane * 16 < pitch) cp_async16(to, src);
+                        if (rowbytes > 512 && k0 + 512 + lane * 16 < pitch)
+                            cp_async16(to + 512, src + 512);
                     }
                     cp_async_arrive(c.bar());
                     c.p.next();
                 }
         }
         for (int i = 0; i < nseg; ++i) {
-            const int step = segs[i].step(S::PANELS);
+            const int step = segs[i].step(c.geo.panels);
             const int stages = (a.d + 255) / 256 * ((segs[i].len / 32 + step - 1) / step);
             for (int q = 0; q < stages; ++q) {
                 if (!c.open()) return false;
@@ -639,7 +677,7 @@ struct Consumer {
     int32_t* flags;
     int32_t* status;
     uint64_t limit;
-    int slot;
+    Geometry geo;
     Ring p;
     bool lost = false;  // a wait ran out: go on without waiting, so that the barriers are met
 
@@ -650,7 +688,7 @@ struct Consumer {
             report_timeout(status);
         }
         lost = __any_sync(0xffffffffu, lost);
-        return ring + (size_t)p.stage * slot;
+        return ring + (size_t)p.stage * geo.slot;
     }
     __device__ __forceinline__ void done() {
         __syncwarp();
@@ -664,7 +702,7 @@ struct Consumer {
 template <int TT>
 __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float* red) {
     using S = Shape<0, TT>;
-    constexpr int NT = S::NT;
+    constexpr int NT = (TT + 7) / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
     const int lm = lane & 7, lq = lane >> 3;         // row and matrix of an ldmatrix address
     // rows of tokens past the expert's repeat its last one: their columns of the
@@ -672,15 +710,15 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
     uint32_t xrow[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-        xrow[nt] = S::XOFF + min(nt * 8 + lm, s.n - 1) * S::XPITCH + (kw * S::KP + lq * 8) * 2;
+        xrow[nt] = c.geo.xoff + min(nt * 8 + lm, s.n - 1) * c.geo.xpitch + (kw * S::KB + lq * 8) * 2;
     float acc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[nt][q] = 0.f;
-    for (int k0 = 0; k0 < d; k0 += S::KA) {
+    for (int k0 = 0; k0 < d; k0 += c.geo.ka) {
         const uint32_t st = smem_addr(c.wait());
-        if (!c.lost && k0 + kw * S::KP < d) {
+        if (!c.lost && k0 + kw * S::KB < d) {
             uint32_t b[NT][2][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -704,6 +742,7 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+        if (nt * 8 >= s.n) break;
         float* q = red + nt * 160 + 2 * (lane & 3) * 20 + (lane >> 2);
         q[0] = acc[nt][0];
         q[20] = acc[nt][1];
@@ -712,16 +751,14 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
     }
 }
 
-// Column c of a tile group of the planes of 8 tokens is token c / 3, plane c % 3:
-// three tiles of 8 columns, of which n tokens use the first 3 n / 8 rounded up.
-__device__ __forceinline__ bool tile_used(int tile, int n) { return tile * 8 < 3 * n; }
-
+// Column c of the products is token c / 3, plane c % 3: n tokens take 3 n / 8 tiles
+// of 8 columns, rounded up.
 // Planes joined: v[tile][4] as the products leave them to y[4], the sums of
 // tokens 2 ft and 2 ft + 1 in the lane's two rows, as a tile of 8 tokens would
 // leave them.  A lane's tokens are columns 6 ft .. 6 ft + 5, in three lanes of a
 // quad; in each round every lane gives one pair of columns and takes one.
 template <int TILES>
-__device__ __forceinline__ void join_planes(const float (&v)[TILES][4], float (&y)[4]) {
+__device__ __forceinline__ void join_planes(const float (*v)[4], float (&y)[4]) {
     const int ft = threadIdx.x & 3;
     float pair[3][4];
 #pragma unroll
@@ -749,74 +786,75 @@ __device__ __forceinline__ void join_planes(const float (&v)[TILES][4], float (&
     }
 }
 
-// The same for 4 bits; TILES: tiles of planes per 8 tokens (1: at most two tokens).
+// The same for 4 bits; TILES: tiles of 8 columns, up to three all computed, so that
+// their products overlap.
 template <int G, int TT, int TILES>
 __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* red) {
     using S = Shape<G, TT>;
-    constexpr int NT = TILES == 1 ? 1 : S::NT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
     const int lm = lane & 7, lq = lane >> 3;
-    uint32_t xrow[NT][TILES];
-    float acc[NT][TILES][4];
+    uint32_t xrow[TILES];
+    float acc[TILES][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int t = 0; t < TILES; ++t) {
+        const int row = min(t * 8 + lm, 3 * s.n - 1);
+        xrow[t] = c.geo.xoff + row * c.geo.xpitch + kw * c.geo.blocks * 128 + lq * 16;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
+    }
+    auto block = [&](const uint8_t* stp, int kb) {
+        const int blk = kw * c.geo.blocks + kb;
+        const uint4* cw = reinterpret_cast<const uint4*>(stp + blk * S::QB + gw * 1024);
+        const uint32_t st = smem_addr(stp);
+        uint32_t f[4][4];
+        {
+            const uint4 lo = cw[lane], hi = cw[32 + lane];
+            codes_to_frag(lo.x, lo.y, f[0]);
+            codes_to_frag(lo.z, lo.w, f[1]);
+            codes_to_frag(hi.x, hi.y, f[2]);
+            codes_to_frag(hi.z, hi.w, f[3]);
+        }
+        const uint32_t sa = st + blk * S::QB + 4096 + (gw * 16 + (lane >> 2)) * 2;
+        float sl[128 / S::GG], sh[128 / S::GG];
+#pragma unroll
+        for (int q = 0; q < 128 / S::GG; ++q) {
+            sl[q] = lds_bf16(sa + q * 128);
+            sh[q] = lds_bf16(sa + q * 128 + 16);
+        }
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const int row = min(nt * 24 + t * 8 + lm, 3 * s.n - 1);
-            xrow[nt][t] = S::XOFF + row * S::XPITCH + kw * S::KP + lq * 16;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[nt][t][q] = 0.f;
-        }
-    for (int k0 = 0; k0 < d; k0 += S::KA) {
-        const uint8_t* stp = c.wait();
-        const uint32_t st = smem_addr(stp);
-#pragma unroll
-        for (int kb = 0; kb < S::KP / 128; ++kb) {
-            if (c.lost || k0 + kw * S::KP + kb * 128 >= d) break;
-            const int blk = kw * (S::KP / 128) + kb;
-            const uint4* cw = reinterpret_cast<const uint4*>(stp + blk * S::QB + gw * 1024);
-            uint32_t f[4][4];
-            {
-                const uint4 lo = cw[lane], hi = cw[32 + lane];
-                codes_to_frag(lo.x, lo.y, f[0]);
-                codes_to_frag(lo.z, lo.w, f[1]);
-                codes_to_frag(hi.x, hi.y, f[2]);
-                codes_to_frag(hi.z, hi.w, f[3]);
-            }
-            const uint32_t sa = st + blk * S::QB + 4096 + (gw * 16 + (lane >> 2)) * 2;
-            float sl[128 / S::GG], sh[128 / S::GG];
+            if (TILES > 3 && t * 8 >= 3 * s.n) break;
+            uint32_t b[2][4];
+            ldmatrix4(st + xrow[t] + kb * 128, b[0]);
+            ldmatrix4(st + xrow[t] + kb * 128 + 64, b[1]);
 #pragma unroll
             for (int q = 0; q < 128 / S::GG; ++q) {
-                sl[q] = lds_bf16(sa + q * 128);
-                sh[q] = lds_bf16(sa + q * 128 + 16);
+                int g[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int u = q * (S::GG / 32); u < (q + 1) * (S::GG / 32); ++u)
+                    imma(g, f[u], b[u / 2][2 * (u & 1)], b[u / 2][2 * (u & 1) + 1]);
+                acc[t][0] = fmaf(small_int(g[0]), sl[q], acc[t][0]);
+                acc[t][1] = fmaf(small_int(g[1]), sl[q], acc[t][1]);
+                acc[t][2] = fmaf(small_int(g[2]), sh[q], acc[t][2]);
+                acc[t][3] = fmaf(small_int(g[3]), sh[q], acc[t][3]);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int t = 0; t < TILES; ++t) {
-                    if (TILES > 1 && !tile_used(t, s.n - 8 * nt)) break;
-                    uint32_t b[2][4];
-                    ldmatrix4(st + xrow[nt][t] + kb * 128, b[0]);
-                    ldmatrix4(st + xrow[nt][t] + kb * 128 + 64, b[1]);
-#pragma unroll
-                    for (int q = 0; q < 128 / S::GG; ++q) {
-                        int g[4] = {0, 0, 0, 0};
-#pragma unroll
-                        for (int u = q * (S::GG / 32); u < (q + 1) * (S::GG / 32); ++u)
-                            imma(g, f[u], b[u / 2][2 * (u & 1)], b[u / 2][2 * (u & 1) + 1]);
-                        acc[nt][t][0] = fmaf(small_int(g[0]), sl[q], acc[nt][t][0]);
-                        acc[nt][t][1] = fmaf(small_int(g[1]), sl[q], acc[nt][t][1]);
-                        acc[nt][t][2] = fmaf(small_int(g[2]), sh[q], acc[nt][t][2]);
-                        acc[nt][t][3] = fmaf(small_int(g[3]), sh[q], acc[nt][t][3]);
-                    }
-                }
+        }
+    };
+    for (int k0 = 0; k0 < d; k0 += c.geo.ka) {
+        const uint8_t* stp = c.wait();
+        const int left = c.lost ? 0 : d - k0 - kw * c.geo.blocks * 128;
+        if (c.geo.blocks == 2 && left > 128) {
+            block(stp, 0);
+            block(stp, 1);
+        } else if (left > 0) {
+            block(stp, 0);
         }
         c.done();
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < (TILES + 2) / 3; ++nt) {
         float y[4];
-        join_planes<TILES>(acc[nt], y);
+        join_planes<(TILES < 3 ? TILES : 3)>(acc + 3 * nt, y);
         float* q = red + nt * 160 + 2 * (lane & 3) * 20 + (lane >> 2);
         q[0] = y[0];
         q[20] = y[1];
@@ -831,7 +869,7 @@ template <int TT>
 __device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool mine, uint32_t hs,
                                           float* out) {
     using S = Shape<0, TT>;
-    constexpr int NT = S::NT;
+    constexpr int NT = (TT + 7) / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
     const int lm = lane & 7, lq = lane >> 3;
     // H fragments: matrices (high, k), (high, k + 8), (low, k), (low, k + 8); one
@@ -840,22 +878,22 @@ __device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool
     float acc[NT][4], low[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        hrow[nt] = hs + (lq >> 1) * S::HPART + min(nt * 8 + lm, s.n - 1) * S::HPITCH +
+        hrow[nt] = hs + (lq >> 1) * c.geo.hpart + min(nt * 8 + lm, s.n - 1) * S::HPITCH +
                    (s.hb + (lq & 1) * 8) * 2;
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[nt][q] = low[nt][q] = 0.f;
     }
-    const int step = s.step(S::PANELS);
+    const int step = s.step(c.geo.panels);
     for (int p0 = 0; p0 < s.len / 32; p0 += step) {
         const int np = min(step, s.len / 32 - p0);
         const uint32_t st = smem_addr(c.wait());
         if (!c.lost && mine) {
 #pragma unroll
-            for (int q = 0; q < S::PANELS; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 if (q >= np) break;
                 // box (q, rb): 128 rows of 64 bytes
                 const uint32_t wa =
-                    st + (q * 2 + rb) * S::ROWBLK + (tile * 16 + (lq & 1) * 8 + lm) * 64;
+                    st + (q * 2 + rb) * S::PANEL + (tile * 16 + (lq & 1) * 8 + lm) * 64;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t f[4];
@@ -895,29 +933,27 @@ template <int G, int TT, int TILES>
 __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool mine, uint32_t hs,
                                         const float* hf, float* out) {
     using S = Shape<G, TT>;
-    constexpr int NT = TILES == 1 ? 1 : S::NT;
+    constexpr int PG = S::GG / 32;  // panels of a group
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
     const int lm = lane & 7, lq = lane >> 3, ft = lane & 3;
-    uint32_t hrow[NT][TILES];
-    float acc[NT][TILES][4];
+    uint32_t hrow[TILES];
+    float acc[TILES][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int t = 0; t < TILES; ++t) {
+        const int row = min(t * 8 + lm, 3 * s.n - 1);
+        hrow[t] = hs + row / 3 * S::HPITCH + row % 3 * S::HPLANE + s.hb + lq * 16;
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-            const int row = min(nt * 24 + t * 8 + lm, 3 * s.n - 1);
-            hrow[nt][t] = hs + row / 3 * S::HPITCH + row % 3 * S::HPLANE + s.hb + lq * 16;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[nt][t][q] = 0.f;
-        }
-    const int step = s.step(S::PANELS);
+        for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
+    }
+    const int step = s.step(c.geo.panels);
     for (int p0 = 0; p0 < s.len / 32; p0 += step) {
         const int np = min(step, s.len / 32 - p0);
         const uint8_t* stp = c.wait();
         if (!c.lost && mine) {
-            constexpr int PG = S::GG / 32;  // panels of a group
             const int first = s.j0 / 32 + p0, q0 = first / PG;
-            const uint2* cw = reinterpret_cast<const uint2*>(stp + rb * S::ROWBLK + tile * 256) + lane;
-            const uint32_t sa = smem_addr(stp) + S::SCALES + rb * S::GROUPS * 256 +
+            const int block = c.geo.panels * S::PANEL, scale = S::groups(c.geo.panels) * 256;
+            const uint2* cw = reinterpret_cast<const uint2*>(stp + rb * block + tile * 256) + lane;
+            const uint32_t sa = smem_addr(stp) + 2 * block + rb * scale +
                                 (tile * 16 + (lane >> 2)) * 2;
             // the panels of one group at a time: their sum is exact
             for (int p = 0; p < np;) {
@@ -926,32 +962,29 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
                 const float sl = lds_bf16(sa + gq * 256), sh = lds_bf16(sa + gq * 256 + 16);
                 uint32_t f[PG][4];
 #pragma unroll
-                for (int i = 0; i < PG; ++i) {
+                for (int i = 0; i < PG; ++i) {  // (a panel past the group: zero codes)
                     const uint2 w = p + i < pe ? cw[(p + i) * 256] : make_uint2(0, 0);
                     codes_to_frag(w.x, w.y, f[i]);
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int t = 0; t < TILES; ++t) {
+                    if (TILES > 3 && t * 8 >= 3 * s.n) break;
+                    int g[2][4];
 #pragma unroll
-                    for (int t = 0; t < TILES; ++t) {
-                        if (TILES > 1 && !tile_used(t, s.n - 8 * nt)) break;
-                        int g[2][4];
+                    for (int q = 0; q < 4; ++q) g[0][q] = g[1][q] = 0;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) g[0][q] = g[1][q] = 0;
-#pragma unroll
-                        for (int i = 0; i < PG; i += 2) {  // an H fragment serves two panels
-                            if (i && p + i >= pe) break;
-                            uint32_t b[4];
-                            ldmatrix4(hrow[nt][t] + (p0 + p + i) * 32, b);
-                            imma(g[0], f[i], b[0], b[1]);
-                            // (a panel past the group has zero codes)
-                            if (PG > 1) imma(g[1], f[(i + 1) % PG], b[2], b[3]);
-                        }
-                        acc[nt][t][0] = fmaf(small_int(g[0][0] + g[1][0]), sl, acc[nt][t][0]);
-                        acc[nt][t][1] = fmaf(small_int(g[0][1] + g[1][1]), sl, acc[nt][t][1]);
-                        acc[nt][t][2] = fmaf(small_int(g[0][2] + g[1][2]), sh, acc[nt][t][2]);
-                        acc[nt][t][3] = fmaf(small_int(g[0][3] + g[1][3]), sh, acc[nt][t][3]);
+                    for (int i = 0; i < PG; i += 2) {  // an H fragment serves two panels
+                        uint32_t b[4];
+                        // (and its second half of the group may lie past the share)
+                        ldmatrix4(hrow[t] + (p0 + (p + i < pe ? p + i : p)) * 32, b);
+                        imma(g[0], f[i], b[0], b[1]);
+                        if (PG > 1) imma(g[1], f[(i + 1) % PG], b[2], b[3]);
                     }
+                    acc[t][0] = fmaf(small_int(g[0][0] + g[1][0]), sl, acc[t][0]);
+                    acc[t][1] = fmaf(small_int(g[0][1] + g[1][1]), sl, acc[t][1]);
+                    acc[t][2] = fmaf(small_int(g[0][2] + g[1][2]), sh, acc[t][2]);
+                    acc[t][3] = fmaf(small_int(g[0][3] + g[1][3]), sh, acc[t][3]);
+                }
                 p = pe;
             }
         }
@@ -959,9 +992,9 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
     }
     if (!mine) return;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < (TILES + 2) / 3; ++nt) {
         float y[4];
-        join_planes<TILES>(acc[nt], y);
+        join_planes<(TILES < 3 ? TILES : 3)>(acc + 3 * nt, y);
         const int n = nt * 8 + 2 * ft;
         float* q = out + (int64_t)n * d;
         if (n < s.n) {
@@ -988,9 +1021,9 @@ __device__ __forceinline__ void digits(float scaled, int8_t (&p)[3]) {
 __device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? 21 - ilogbf(m) : 0; }
 
 template <int G, int TT>
-__device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring, int slot,
-                        int stages, uint64_t* full, uint64_t* empty, uint8_t* Hs, float* red,
-                        float (*hf)[FT], int32_t* flags) {
+__device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring,
+                        const Geometry& geo, uint64_t* full, uint64_t* empty, uint8_t* Hs,
+                        float* red, float (*hf)[FT], int32_t* flags) {
     using S = Shape<G, TT>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gw = warp >> 2, gt = tid & 127;  // group of four warps; thread of the group
@@ -1002,8 +1035,8 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
     c.flags = flags;
     c.status = a.status;
     c.limit = a.wait_limit_ns;
-    c.slot = slot;
-    c.p.stages = stages;
+    c.geo = geo;
+    c.p.stages = geo.stages;
     int turn = 0;  // which half of red
     for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
         named_sync(1, CONSUMERS);  // the last part's shares and H have been read
@@ -1020,21 +1053,25 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
             const float gate = n < s.n ? r.gate[s.item][n] : 0.f;
             const float xf = S::Q4 && n < s.n ? a.xf[r.tok[s.item][n]] : 1.f;
             for (int j = 0; j < s.len; j += FEW_GRAN, turn ^= 1) {
-                float* base = red + turn * (S::RED / 8);
-                float* mine = base + warp * (S::NT * 160);
+                float* base = red + turn * (16 * geo.nt * 160);
+                float* mine = base + warp * (geo.nt * 160);
                 if constexpr (!S::Q4)
                     up_bf16<TT>(c, s, d, mine);
                 else if (TT <= 2 || s.n <= 2)
                     up_q4<G, TT, 1>(c, s, d, mine);
+                else if (s.n <= 5)
+                    up_q4<G, TT, TT <= 2 ? 1 : 2>(c, s, d, mine);
+                else if (TT <= 8 || s.n <= 8)
+                    up_q4<G, TT, TT <= 2 ? 1 : 3>(c, s, d, mine);
                 else
-                    up_q4<G, TT, 3>(c, s, d, mine);
+                    up_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 3 : 6>(c, s, d, mine);
                 named_sync(2 + gw, 128);
                 if (n < s.n) {
                     float ga = 0.f, up = 0.f;
 #pragma unroll
                     for (int w = 0; w < S::KW; ++w) {
                         // (a tile of 8 tokens is 160 floats)
-                        const float* q = base + (gw * 4 + w) * (S::NT * 160) + n * 20 + jj;
+                        const float* q = base + (gw * 4 + w) * (geo.nt * 160) + n * 20 + jj;
                         ga += q[0];
                         up += q[8];
                     }
@@ -1046,7 +1083,7 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                         __nv_bfloat16* H = reinterpret_cast<__nv_bfloat16*>(Hs + n * S::HPITCH);
                         const float hi = bf16_round(hv);
                         H[at] = __float2bfloat16_rn(hi);
-                        H[S::HPART / 2 + at] = __float2bfloat16_rn(hv - hi);
+                        H[geo.hpart / 2 + at] = __float2bfloat16_rn(hv - hi);
                     }
                 }
             }
@@ -1102,8 +1139,12 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                     down_bf16<TT>(c, s, d, mine, hs, out);
                 else if (TT <= 2 || s.n <= 2)
                     down_q4<G, TT, 1>(c, s, d, mine, hs, hf[i], out);
+                else if (s.n <= 5)
+                    down_q4<G, TT, TT <= 2 ? 1 : 2>(c, s, d, mine, hs, hf[i], out);
+                else if (TT <= 8 || s.n <= 8)
+                    down_q4<G, TT, TT <= 2 ? 1 : 3>(c, s, d, mine, hs, hf[i], out);
                 else
-                    down_q4<G, TT, 3>(c, s, d, mine, hs, hf[i], out);
+                    down_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 3 : 6>(c, s, d, mine, hs, hf[i], out);
             }
         }
     }
@@ -1112,15 +1153,12 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
 template <int G, int TT>
 __global__ void __launch_bounds__(FFN_THREADS, 1)
     few_ffn_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a,
-                   int slot, int stages) {
+                   int bytes) {
     using S = Shape<G, TT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + (-smem_addr(smem_raw) & 1023);
-    uint8_t* Hs = ring + (size_t)slot * stages;
-    float* red = reinterpret_cast<float*>(Hs + (S::HBYTES + 15) / 16 * 16);
-    Routing& r = *reinterpret_cast<Routing*>(reinterpret_cast<uint8_t*>(red) + S::RED);
-    uint64_t* full = reinterpret_cast<uint64_t*>(
-        reinterpret_cast<uint8_t*>(&r) + (sizeof(Routing) + 15) / 16 * 16);
+    Routing& r = *reinterpret_cast<Routing*>(ring + bytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + bytes + (sizeof(Routing) + 15) / 16 * 16);
     uint64_t* empty = full + MAX_STAGES;
     // a wait ran out; stages issued; shares of the part
     int32_t* flags = reinterpret_cast<int32_t*>(empty + MAX_STAGES);
@@ -1130,7 +1168,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     for (int e = tid; e < MAX_E; e += FFN_THREADS) r.tokens[e] = 0;
     if (tid < MAX_E / 32) r.hit[tid] = 0;
     if (tid == 0) {
-        for (int i = 0; i < stages; ++i) {
+        for (int i = 0; i < MAX_STAGES; ++i) {
             // the weights' announcement and the token warps' lanes
             mbar_init(&full[i], 1 + TOKEN_WARPS * 32);
             mbar_init(&empty[i], CONSUMERS / 32);
@@ -1146,8 +1184,10 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     __syncthreads();
     pdl_wait();  // the router's logits (and planes)
     route_batch(a, r);
+    const Geometry geo = geometry<S>(r.most, bytes);
     if (warp < CONSUMERS / 32) {
-        consume<G, TT>(a, r, segs[0], ring, slot, stages, full, empty, Hs, red, hf, flags);
+        consume<G, TT>(a, r, segs[0], ring, geo, full, empty, ring + geo.h,
+                       reinterpret_cast<float*>(ring + geo.red), hf, flags);
     } else if (!(a.test_stall && blockIdx.x == 0)) {
         // (with the test hook nothing is brought in: the consumers' waits run out)
         Bringer c;
@@ -1155,8 +1195,8 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         c.full = full;
         c.empty = empty;
         c.limit = a.wait_limit_ns;
-        c.slot = slot;
-        c.p.stages = stages;
+        c.geo = geo;
+        c.p.stages = geo.stages;
         const int w = warp - CONSUMERS / 32;
         const bool ok = w == 0 ? bring_weights<G, TT>(a, r, maps, segs[1], c, &flags[1])
                                : bring_tokens<G, TT>(a, r, segs[1 + w], c, w - 1);
@@ -1167,9 +1207,9 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     __syncthreads();
     if (flags[0] && tid == 0) {
         // a wait ran out: see the copies in flight land before the block goes
-        const int n = flags[1];
-        for (int i = n > stages ? n - stages : 0; i < n; ++i)
-            mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1, a.wait_limit_ns);
+        const int n = flags[1], m = geo.stages;
+        for (int i = n > m ? n - m : 0; i < n; ++i)
+            mbar_wait(&full[i % m], (uint32_t)(i / m) & 1, a.wait_limit_ns);
     }
 }
 
@@ -1383,20 +1423,17 @@ void router_launch(const FewArgs& a, const float* Wr, float* z, cudaStream_t st)
 
 template <int G, int TT>
 int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
-    using S = Shape<G, TT>;
-    const int slot = S::slot(a.T);
     // the kernel's few static bytes count too
-    const size_t limit =
-        (size_t)smem_limit - (2 + TOKEN_WARPS) * MAX_SEGS * sizeof(Seg) -
-        MAX_SEGS * FT * sizeof(float) - 256;
-    int stages = (int)((limit - S::fixed()) / slot);
-    stages = stages > MAX_STAGES ? MAX_STAGES : stages;
-    const size_t smem = S::fixed() + (size_t)slot * stages;
+    const size_t limit = (size_t)smem_limit - (2 + TOKEN_WARPS) * MAX_SEGS * sizeof(Seg) -
+                         MAX_SEGS * FT * sizeof(float) - 256;
+    // (1 KB to align the ring, the routing and the barriers behind the rest)
+    const size_t fixed = 1024 + (sizeof(Routing) + 15) / 16 * 16 + 2 * MAX_STAGES * 8 + 16;
+    const int bytes = (int)((limit - fixed) / 1024 * 1024);
     auto kern = few_ffn_kernel<G, TT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) !=
         cudaSuccess)
         return launch_result();
-    launch_ex(true, kern, dim3(FEW_CTAS), dim3(FFN_THREADS), smem, st, m, a, slot, stages);
+    launch_ex(true, kern, dim3(FEW_CTAS), dim3(FFN_THREADS), fixed + bytes, st, m, a, bytes);
     note_launch();
     return launch_result();
 }
