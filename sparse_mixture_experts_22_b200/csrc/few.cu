@@ -177,7 +177,7 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
     __syncthreads();
     // two prefixes over the items: weighted granules, then tokens x parts
     if (tid < 32) {
-        int before = 0, heaviest = 0, most = 0;
+        int before = 0, heaviest = 0, lightest = 1 << 30, most = 0;
         for (int i0 = 0; i0 < items; i0 += 32) {
             const int i = i0 + tid;
             const int cost = i < items ? few_cost(a.G, r.n[i]) : 0;
@@ -189,12 +189,14 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
             heaviest = max(heaviest, (int)__reduce_max_sync(0xffffffffu, (unsigned)cost));
+            lightest = min(lightest,
+                           (int)__reduce_min_sync(0xffffffffu, i < items ? (unsigned)cost : 1u << 30));
             most = max(most, (int)__reduce_max_sync(0xffffffffu, i < items ? (unsigned)r.n[i] : 0u));
         }
         if (tid == 0) {
             r.most = most;
             r.W = before;
-            r.V = few_parts(before, heaviest, gridDim.x);
+            r.V = few_parts(before, lightest, heaviest, gridDim.x);
         }
         __syncwarp();
         before = 0;
@@ -422,14 +424,14 @@ __device__ __forceinline__ Geometry geometry(int tokens, int bytes) {
 #pragma unroll
     for (int blocks = S::Q4 ? 2 : 1; blocks >= 1; --blocks) {
         g.blocks = blocks;
-        g.panels = S::Q4 ? 4 * blocks : 2;
+        g.panels = S::Q4 ? 8 : 2;
         g.ka = S::KW * S::KB * blocks;
         g.xpitch = g.ka * S::XBYTES + 16;
         g.xoff = S::Q4 ? g.ka / 128 * S::QB : g.ka * 128;
         const int up = g.xoff + tokens * S::XROWS * g.xpitch;
         g.slot = (max(up, S::down(g.panels)) + 1023) / 1024 * 1024;
         g.stages = min(ring / g.slot, MAX_STAGES);
-        if (g.stages >= 4) break;
+        if (g.stages >= 3) break;
     }
     g.h = g.stages * g.slot;
     g.red = g.h + h;
@@ -1448,20 +1450,22 @@ int launch_ffn_tokens(const FewMaps& m, const FewArgs& a, int smem_limit, cudaSt
 }  // namespace
 
 int64_t few_part_rows(int G, int T, int h, int E, int k, int hsum) {
-    // Parts are at least W / V long rounded down, and no shorter than the costliest
-    // granule, so an item of weight w meets at most w V / W + 2 of them; n tokens
-    // then take n w V / W + 2 n rows.  The sum over the items of n w is at most T W,
-    // and at most (greatest cost / least cost) times what equal costs would make it.
+    // A part is W / V long or one more, rounded down, so an item of weight w meets at
+    // most w / (W / V) + 2 parts; n tokens then take n w / (W / V) + 2 n rows.  The sum
+    // over the items of n w is at most T W, and at most (greatest cost / least cost)
+    // times what equal costs would make it.  V follows from the most that A experts with
+    // N assignments can weigh.
     const int least = few_cost(G, 1), most = few_cost(G, T);
     const int64_t gE = h / FEW_GRAN, gS = hsum / FEW_GRAN, N = (int64_t)T * k;
     int64_t rows = 0;
     for (int64_t A = k; A <= (E < N ? E : N); ++A) {
         const int64_t tot = A * gE + gS;
-        const int64_t V = few_parts((int)(tot * most), least, FEW_CTAS);
+        const int64_t W = 8 * tot + (5 * (gE * (N - A) + gS * (T - 1)) + 1) / 2;
+        const int64_t V = few_parts((int)W, least, 1, FEW_CTAS);
         const int64_t even = (N * gE + T * gS) * V / tot + 1;  // sum of n w V / W at equal costs
         const int64_t skewed = even * most / least + 1, all = T * V;
-        // (rounding W / V down lengthens w V / W by less than one part in 15)
-        const int64_t need = (skewed < all ? skewed : all) * 16 / 15 + 2 * (N + T);
+        // (rounding W / V down lengthens it by one part in W / V, which is at least 8)
+        const int64_t need = (skewed < all ? skewed : all) * 9 / 8 + 2 * (N + T);
         rows = need > rows ? need : rows;
     }
     return rows;

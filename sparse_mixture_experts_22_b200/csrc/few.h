@@ -51,20 +51,26 @@ int launch_q4_dequantize(const void* Q13, const void* Q2, void* W13, void* W2p, 
 
 // ---------------------------------------------------------------- the layer
 
-// What a granule costs an SM when its expert serves n tokens, in eighths of
-// bringing it in: where products take longer than HBM, a part holds fewer granules.
+// What a granule costs an SM when its expert serves n tokens, in eighths of what it
+// costs at one or two: where products take longer than HBM, a part holds fewer
+// granules.  With n tokens for every expert (d = 4096, h = 14336) a granule and SM takes,
+// in us, bf16 17.4 (n <= 2), 18.2 (4), 19.4 (8), 24.2 (16) and 4 bits 6.8-7.4, 9.9-11.8,
+// 15.3-18.6, 30.5-35.2; the costs are about half way between equal and these, because
+// experts with few tokens find more of HBM's rate free beside the others (16 tokens over
+// 8 experts, three draws: 242, 218, 221 us with the full ratios, 236, 203, 215 with
+// these).  At most 8 + 5/2 (n - 1), which few_part_rows counts on.
 __host__ __device__ inline int few_cost(int G, int n) {
-    if (G == 0 || n <= 2) return 8;
-    return n <= 5 ? 9 : n <= 8 ? 12 : 20;
+    if (G == 0) return n <= 8 ? 8 : 10;
+    return n <= 2 ? 8 : n <= 5 ? 10 : n <= 8 ? 14 : n <= 12 ? 19 : 24;
 }
 
 // Parts the experts' hidden units are cut into: W weighted granules in item order
 // (hit experts ascending, then the shared one) over V parts of W / V or one more;
 // every CTA of the grid takes the same number of parts within one, none holds more
-// than FEW_HCAP hidden units (a granule costs 8 at least, and one may begin at the
-// very end), and none is shorter than the costliest granule.
-__host__ __device__ inline int few_parts(int W, int heaviest, int ctas) {
-    const int per = ctas * (FEW_HCAP / FEW_GRAN - 1) * 8;
+// than FEW_HCAP hidden units (one granule less, as one may begin at the very end), and
+// none is shorter than the costliest granule.
+__host__ __device__ inline int few_parts(int W, int lightest, int heaviest, int ctas) {
+    const int per = ctas * (FEW_HCAP / FEW_GRAN - 1) * lightest;
     const int V = ctas * ((W + per - 1) / per), most = W / heaviest;
     return V < most ? V : most;
 }

@@ -29,22 +29,23 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
-// Codes of eight weights, nibble e = q of element e in two's complement.  q =
-// rint(w / s) without eight divisions: w inv is within 2^-20 of the quotient, and
-// as w and s have 8 significant bits and |w / s| <= 7.03, the quotient is either
-// n + 1/2 exactly or at least 2^-10 away from it; the exact remainder tells the
-// half and sends it to the even code.
+// Codes of eight weights, nibble e = q of element e in two's complement.  q = rint(w
+// / s) without divisions or conversions: w inv + 1.5 2^23 leaves the nearest integer
+// in the low bits, and w inv is within 2^-20 of the quotient.  As w and s have 8
+// significant bits and |w / s| <= 7.03 (so that nothing clips), the quotient is either
+// n + 1/2 exactly or at least 2^-10 away from it; the exact remainder tells the half
+// and sends it to the even code.
 __device__ __forceinline__ uint32_t codes_of(const float* w, float s) {
     uint32_t out = 0;
     if (s >= 1.1754944e-38f) {
         const float inv = 1.f / s, half = 0.5f * s;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float q = rintf(w[e] * inv);
-            const float rest = fmaf(-q, s, w[e]);
-            int code = (int)q;
+            const float t = fmaf(w[e], inv, 12582912.f);
+            const float rest = fmaf(12582912.f - t, s, w[e]);
+            uint32_t code = __float_as_uint(t);
             if (fabsf(rest) == half && (code & 1)) code += rest > 0.f ? 1 : -1;
-            out |= (uint32_t)(min(max(code, -7), 7) & 15) << (4 * e);
+            out |= (code & 15) << (4 * e);
         }
     } else {  // no scale, or one below the normal range
 #pragma unroll

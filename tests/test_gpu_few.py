@@ -32,6 +32,10 @@ CASES = {
     # more hidden units than the parts hold at once
     "long_h": Workload("f_long_h", T=11, d=128, h=10240, E=8, k=8),
     "long_d": Workload("f_long_d", T=2, d=8192, h=128, E=2, k=1),
+    # many stages a granule and several granules a part, experts of very different loads
+    "uneven": Workload("f_uneven", T=16, d=2048, h=1024, E=7, k=3, n_shared=1, h_shared=512,
+                       zipf_s=1.5),
+    "deep": Workload("f_deep", T=6, d=4096, h=1408, E=4, k=4),
 }
 
 _made = {}
