@@ -468,10 +468,10 @@ MOE_API int moe_route_static(const moe_config* cfg, const void* x, const float* 
  * moe_forward computes, from the same packed weights, as one pass over the
  * weights of the experts the batch hits [only the chosen experts are computed:
  * Mixtral 8x7B and MoE explained, "Easy explanation" ¶4].  Arguments as in
- * moe_forward, without slot_of; stats may be NULL (two launches less).  H stays
- * on the chip and reaches the down projection as two bf16 parts whatever
- * cfg->hidden_mode says.  Routing outputs equal moe_forward's (gates to fp32
- * rounding); repeated calls give identical bits.
+ * moe_forward, without slot_of; three launches, and two more with stats (which
+ * may be NULL).  H stays on the chip and reaches the down projection as two bf16
+ * parts whatever cfg->hidden_mode says.  Routing outputs equal moe_forward's
+ * (gates to fp32 rounding); repeated calls give identical bits.
  * Errors besides those of every call, before any launch: MOE_ERR_SHAPE for
  * T > MOE_FEW_MAX_T, MOE_ERR_DTYPE for an fp32 config, MOE_ERR_UNSUPPORTED for
  * the reroute policy or train = 1.  ws: moe_few_workspace_size(cfg) bytes,
@@ -503,9 +503,12 @@ MOE_API int moe_q4_dequantize(const moe_config* cfg, int which, int32_t group, c
                               const void* Q2, void* W13, void* W2p, void* stream);
 
 /* moe_forward_few on 4-bit weights (Q13s / Q2s: the shared set, NULL without
- * shared experts).  The products take the values q s exactly (q in bf16, the
- * group's scale in fp32 on its partial sum); nothing is rounded that
- * moe_forward_few does not round.  MOE_ERR_ARG for another group. */
+ * shared experts).  The products take the values q s exactly: sums within a
+ * group are exact integers, the group's scale multiplies them in fp32.  A token's
+ * x enters rounded to 2^-22 of its largest magnitude, and so does H (per token,
+ * expert and the units one SM holds).  A token whose x, or whose H in some expert
+ * it uses, is infinite or NaN gets NaN in its row of out; the other rows do not
+ * change.  MOE_ERR_ARG for another group. */
 MOE_API int moe_forward_few_q4(const moe_config* cfg, int32_t group, const void* x,
                                const float* Wr, const float* bias, const void* Q13,
                                const void* Q2, const void* Q13s, const void* Q2s, void* out,
@@ -524,8 +527,8 @@ MOE_API int moe_read_device_status(const void* ws, int32_t* status, void* stream
  * launches in between). */
 MOE_API int moe_launch_count(uint64_t* n);
 
-/* Programmatic dependent launch inside moe_forward (default on): the
- * kernels of the layer's chain may start while their predecessor finishes,
+/* Programmatic dependent launch inside moe_forward and the few-token calls
+ * (default on): the kernels of the layer's chain may start while their predecessor finishes,
  * each waiting on the device before it reads what the predecessor writes, and
  * the swapped gate/up GEMM prefetches its first weight tiles into L2 while the
  * routing runs.  Results are identical either way.  Process-wide. */
@@ -580,7 +583,8 @@ MOE_API int moe_set_wait_limit_ns(uint64_t ns);
  * after the wait limit (set a short one with moe_set_wait_limit_ns) the
  * kernel records MOE_ERR_TIMEOUT, drains its in-flight copies and MMAs,
  * releases tensor memory and returns.  Results of such a call are garbage;
- * the device stays usable.  Process-wide. */
+ * the device stays usable.  In the few-token calls block 0 of the expert kernel
+ * brings no weights or tokens in, with the same outcome.  Process-wide. */
 MOE_API int moe_set_test_stall(int on);
 
 /* Per-kernel timing of moe_forward.  moe_trace_begin(n, only) records CUDA

@@ -1882,13 +1882,13 @@ static int few_forward(const moe_config* cfg, int32_t group, const void* x, cons
         if (P.S > 0) MOE_TRY(few_maps(&maps.w13s, &maps.w2s, w13s, w2s, 1, P.hsum, P.d));
     }
     trace_pre(st, "few_router");
-    MOE_TRY(launched(launch_few_router(a, Wr, at<float>(ws, F.off_logits), st), "few_router"));
+    MOE_TRY(launched(launch_few_router(a, Wr, at<float>(ws, F.off_logits), g_pdl_enabled, st), "few_router"));
     trace_mark(st, "few_router");
     trace_pre(st, "few_ffn");
-    MOE_TRY(launched(launch_few_ffn(maps, a, dv.smem_optin, st), "few_ffn"));
+    MOE_TRY(launched(launch_few_ffn(maps, a, dv.smem_optin, g_pdl_enabled, st), "few_ffn"));
     trace_mark(st, "few_ffn");
     trace_pre(st, "few_combine");
-    MOE_TRY(launched(launch_few_combine(a, st), "few_combine"));
+    MOE_TRY(launched(launch_few_combine(a, g_pdl_enabled, st), "few_combine"));
     trace_mark(st, "few_combine");
     if (stats) {
         // the full softmax's sums, from the top-k kernel of moe_route on the same

@@ -410,9 +410,10 @@ struct Geometry {
 
 constexpr int MAX_STAGES = 12;
 
-// 4 bits: stages of two blocks and eight panels where four of them fit, else half of
-// that: fewer stages are fewer waits (decode layer, one token: 54.6 us against 63.8),
-// but one of them is being read, and what the others hold has to cover HBM's latency.
+// 4 bits: stages of two blocks of columns where three of them fit, else of one: fewer
+// stages are fewer waits (one token, d = 4096, h = 14336, 2 of 8 experts: 54.6 us
+// against 63.8), but one of them is being read, and what the others hold has to cover
+// HBM's latency.  Eight panels always: four were slower at every size tried.
 template <typename S>
 __device__ __forceinline__ Geometry geometry(int tokens, int bytes) {
     Geometry g;
@@ -753,8 +754,8 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
     }
 }
 
-// Column c of the products is token c / 3, plane c % 3: n tokens take 3 n / 8 tiles
-// of 8 columns, rounded up.
+// Column c of the 4-bit products is token c / 3, plane c % 3: n tokens take 3 n / 8
+// tiles of 8 columns, rounded up.
 // Planes joined: v[tile][4] as the products leave them to y[4], the sums of
 // tokens 2 ft and 2 ft + 1 in the lane's two rows, as a tile of 8 tokens would
 // leave them.  A lane's tokens are columns 6 ft .. 6 ft + 5, in three lanes of a
@@ -1219,33 +1220,36 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
 
 // out[t][c] = sum over the uses of token t (choices in order, then the shared
 // expert) and their parts of the partial rows.  A block takes 32 columns of one
-// token: 32 groups of 8 lanes share the rows, so that most of them are in flight at
-// once (a token of a small batch has as many rows as there are parts).
+// token: 16 groups of 8 lanes share the rows, so that many of them are in flight at
+// once (a token of a small batch has as many rows as there are parts).  128 threads
+// of 32 registers and little shared memory find room beside the expert kernel's
+// block, so that they are there when it ends (8 tokens over 160 experts, d = 5120: the
+// layer 336.7 us with blocks of 256 threads that do not, 324.5 with these; 16 tokens
+// and 4 bits, d = 4096: 242.7 and 232.7).
 constexpr int CB_COLS = 32;
+constexpr int CB_GROUPS = 16;
 
-__global__ void __launch_bounds__(256) few_combine_kernel(const __grid_constant__ FewArgs a) {
-    __shared__ float4 sums[32][9];
+__global__ void __launch_bounds__(CB_GROUPS * 8, 16)
+    few_combine_kernel(const int4* __restrict__ table, const float* __restrict__ part,
+                       __nv_bfloat16* __restrict__ out, int d, int k, int uses) {
+    __shared__ float4 sums[CB_GROUPS][9];
     const int tid = threadIdx.x, col = tid & 7, grp = tid >> 3;
-    const int t = blockIdx.y, c = blockIdx.x * CB_COLS + col * 4;
+    const int t = blockIdx.y;
+    part += blockIdx.x * CB_COLS + col * 4;
     pdl_wait();
-    int4 use[MAX_K + 1];
-#pragma unroll
-    for (int j = 0; j <= MAX_K; ++j)
-        use[j] = j < a.k + (a.hsum > 0) ? a.table[t * (a.k + 1) + j] : make_int4(0, 0, 0, 0);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     int at = grp;  // this group's place among the rows of the use
-#pragma unroll
-    for (int j = 0; j <= MAX_K; ++j) {
+    for (int j = 0; j < uses; ++j) {
+        const int4 u = table[t * (k + 1) + j];
 #pragma unroll 4
-        for (; at < use[j].y; at += 32) {
-            const float4 v = *reinterpret_cast<const float4*>(
-                a.part + (int64_t)(use[j].x + at * use[j].z) * a.d + c);
+        for (; at < u.y; at += CB_GROUPS) {
+            const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)(u.x + at * u.z) * d);
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
         }
-        at -= use[j].y;
+        at -= u.y;
     }
     sums[grp][col] = s;
     __syncthreads();
@@ -1253,11 +1257,10 @@ __global__ void __launch_bounds__(256) few_combine_kernel(const __grid_constant_
         const float* q = reinterpret_cast<const float*>(sums) + tid;
         float o = 0.f;
 #pragma unroll
-        for (int g = 0; g < 32; ++g) o += q[g * 36];
+        for (int g = 0; g < CB_GROUPS; ++g) o += q[g * 36];
         const float hi = __shfl_down_sync(0xffffffffu, o, 1);
         if ((tid & 1) == 0)
-            *reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                         (int64_t)t * a.d + blockIdx.x * CB_COLS + tid) =
+            *reinterpret_cast<uint32_t*>(out + (int64_t)t * d + blockIdx.x * CB_COLS + tid) =
                 pack_bf16x2(o, hi);
     }
 }
@@ -1339,7 +1342,8 @@ __global__ void __cluster_dims__(1, RC, 1) __launch_bounds__(ROUTER_THREADS)
     __shared__ float sum[TT * 8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int d = a.d, E = a.E, T = a.T;
-    pdl_trigger();
+    pdl_trigger();  // (the expert kernel reads no memory before its own wait)
+    pdl_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *a.status = DEV_OK;
     if ((int)blockIdx.x == (E + 7) / 8) {
         split_planes(a);
@@ -1417,16 +1421,16 @@ __global__ void __cluster_dims__(1, RC, 1) __launch_bounds__(ROUTER_THREADS)
 }
 
 template <int TT>
-void router_launch(const FewArgs& a, const float* Wr, float* z, cudaStream_t st) {
+void router_launch(const FewArgs& a, const float* Wr, float* z, bool pdl, cudaStream_t st) {
     const dim3 grid((a.E + 7) / 8 + (a.G > 0), RC);
-    if (a.E % 4 == 0) few_router_kernel<TT, true><<<grid, ROUTER_THREADS, 0, st>>>(a, Wr, z);
-    else few_router_kernel<TT, false><<<grid, ROUTER_THREADS, 0, st>>>(a, Wr, z);
+    launch_ex(pdl, a.E % 4 == 0 ? few_router_kernel<TT, true> : few_router_kernel<TT, false>, grid,
+              dim3(ROUTER_THREADS), 0, st, a, Wr, z);
 }
 
 template <int G, int TT>
-int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
-    // the kernel's few static bytes count too
-    const size_t limit = (size_t)smem_limit - (2 + TOKEN_WARPS) * MAX_SEGS * sizeof(Seg) -
+int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, bool pdl, cudaStream_t st) {
+    // the kernel's few static bytes count too, and a block of the combine finds 4 KB
+    const size_t limit = (size_t)smem_limit - 4096 - (2 + TOKEN_WARPS) * MAX_SEGS * sizeof(Seg) -
                          MAX_SEGS * FT * sizeof(float) - 256;
     // (1 KB to align the ring, the routing and the barriers behind the rest)
     const size_t fixed = 1024 + (sizeof(Routing) + 15) / 16 * 16 + 2 * MAX_STAGES * 8 + 16;
@@ -1435,16 +1439,17 @@ int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t 
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) !=
         cudaSuccess)
         return launch_result();
-    launch_ex(true, kern, dim3(FEW_CTAS), dim3(FFN_THREADS), fixed + bytes, st, m, a, bytes);
+    launch_ex(pdl, kern, dim3(FEW_CTAS), dim3(FFN_THREADS), fixed + bytes, st, m, a, bytes);
     note_launch();
     return launch_result();
 }
 
 template <int G>
-int launch_ffn_tokens(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
-    if (G && a.T <= 2) return launch_ffn<G, G ? 2 : 8>(m, a, smem_limit, st);
-    if (a.T <= 8) return launch_ffn<G, 8>(m, a, smem_limit, st);
-    return launch_ffn<G, 16>(m, a, smem_limit, st);
+int launch_ffn_tokens(const FewMaps& m, const FewArgs& a, int smem_limit, bool pdl,
+                      cudaStream_t st) {
+    if (G && a.T <= 2) return launch_ffn<G, G ? 2 : 8>(m, a, smem_limit, pdl, st);
+    if (a.T <= 8) return launch_ffn<G, 8>(m, a, smem_limit, pdl, st);
+    return launch_ffn<G, 16>(m, a, smem_limit, pdl, st);
 }
 
 }  // namespace
@@ -1471,26 +1476,29 @@ int64_t few_part_rows(int G, int T, int h, int E, int k, int hsum) {
     return rows;
 }
 
-int launch_few_router(const FewArgs& a, const float* Wr, float* z, cudaStream_t st) {
-    if (a.T == 1) router_launch<1>(a, Wr, z, st);
-    else if (a.T <= 4) router_launch<4>(a, Wr, z, st);
-    else if (a.T <= 8) router_launch<8>(a, Wr, z, st);
-    else router_launch<16>(a, Wr, z, st);
+int launch_few_router(const FewArgs& a, const float* Wr, float* z, bool pdl, cudaStream_t st) {
+    if (a.T == 1) router_launch<1>(a, Wr, z, pdl, st);
+    else if (a.T <= 4) router_launch<4>(a, Wr, z, pdl, st);
+    else if (a.T <= 8) router_launch<8>(a, Wr, z, pdl, st);
+    else router_launch<16>(a, Wr, z, pdl, st);
     note_launch();
     return launch_result();
 }
 
-int launch_few_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st) {
+int launch_few_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, bool pdl,
+                   cudaStream_t st) {
     switch (a.G) {
-        case 0: return launch_ffn_tokens<0>(m, a, smem_limit, st);
-        case 32: return launch_ffn_tokens<32>(m, a, smem_limit, st);
-        case 64: return launch_ffn_tokens<64>(m, a, smem_limit, st);
-        default: return launch_ffn_tokens<128>(m, a, smem_limit, st);
+        case 0: return launch_ffn_tokens<0>(m, a, smem_limit, pdl, st);
+        case 32: return launch_ffn_tokens<32>(m, a, smem_limit, pdl, st);
+        case 64: return launch_ffn_tokens<64>(m, a, smem_limit, pdl, st);
+        default: return launch_ffn_tokens<128>(m, a, smem_limit, pdl, st);
     }
 }
 
-int launch_few_combine(const FewArgs& a, cudaStream_t st) {
-    launch_ex(true, few_combine_kernel, dim3(a.d / CB_COLS, a.T), dim3(256), 0, st, a);
+int launch_few_combine(const FewArgs& a, bool pdl, cudaStream_t st) {
+    launch_ex(pdl, few_combine_kernel, dim3(a.d / CB_COLS, a.T), dim3(CB_GROUPS * 8), 0, st,
+              (const int4*)a.table, (const float*)a.part, reinterpret_cast<__nv_bfloat16*>(a.out), a.d,
+              a.k, a.k + (a.hsum > 0));
     note_launch();
     return launch_result();
 }

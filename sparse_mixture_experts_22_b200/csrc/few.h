@@ -105,7 +105,7 @@ struct FewArgs {
 int64_t few_part_rows(int G, int T, int h, int E, int k, int hsum);
 // Logits z [T][E] = x Wr; clears the status word; with 4-bit weights (a.G) also
 // splits x into its planes.
-int launch_few_router(const FewArgs& a, const float* Wr, float* z, cudaStream_t st);
+int launch_few_router(const FewArgs& a, const float* Wr, float* z, bool pdl, cudaStream_t st);
 // Tensor maps of the bf16 weights (unused with 4 bits): W13 as [blocks of 128
 // rows][128][d] in boxes of 64 columns x 32 rows x 2 blocks (a granule's gate
 // and up rows) with the 128-byte swizzle, W2p as rows of the hidden width in
@@ -113,7 +113,7 @@ int launch_few_router(const FewArgs& a, const float* Wr, float* z, cudaStream_t 
 struct FewMaps {
     CUtensorMap w13, w2, w13s, w2s;
 };
-int launch_few_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, cudaStream_t st);
-int launch_few_combine(const FewArgs& a, cudaStream_t st);
+int launch_few_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, bool pdl, cudaStream_t st);
+int launch_few_combine(const FewArgs& a, bool pdl, cudaStream_t st);
 
 }  // namespace moe

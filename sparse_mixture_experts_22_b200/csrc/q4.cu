@@ -31,14 +31,14 @@ __device__ __forceinline__ float group_max(float v) {
 
 // Codes of eight weights, nibble e = q of element e in two's complement.  q = rint(w
 // / s) without divisions or conversions: w inv + 1.5 2^23 leaves the nearest integer
-// in the low bits, and w inv is within 2^-20 of the quotient.  As w and s have 8
-// significant bits and |w / s| <= 7.03 (so that nothing clips), the quotient is either
-// n + 1/2 exactly or at least 2^-10 away from it; the exact remainder tells the half
-// and sends it to the even code.
+// in the low bits, and w inv is within 2^-19 of the quotient (the fast reciprocal is
+// off by 2 ulp).  As w and s have 8 significant bits and |w / s| <= 7.03 (so that
+// nothing clips), the quotient is either n + 1/2 exactly or at least 2^-10 away from
+// it; the exact remainder tells the half and sends it to the even code.
 __device__ __forceinline__ uint32_t codes_of(const float* w, float s) {
     uint32_t out = 0;
-    if (s >= 1.1754944e-38f) {
-        const float inv = 1.f / s, half = 0.5f * s;
+    if (s >= 1.1754944e-38f && s <= 8.5070592e37f) {  // (the fast reciprocal's range)
+        const float inv = __fdividef(1.f, s), half = 0.5f * s;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float t = fmaf(w[e], inv, 12582912.f);
@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t codes_of(const float* w, float s) {
             if (fabsf(rest) == half && (code & 1)) code += rest > 0.f ? 1 : -1;
             out |= (code & 15) << (4 * e);
         }
-    } else {  // no scale, or one below the normal range
+    } else {  // no scale, or one at the end of the range
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float q = s > 0.f ? rintf(w[e] / s) : 0.f;

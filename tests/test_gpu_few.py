@@ -298,6 +298,74 @@ def test_graph_replay_gives_the_eager_bits(group):
     del graph
 
 
+@pytest.mark.parametrize("pdl", [True, False])
+@pytest.mark.parametrize("group", [0, 32])
+def test_steps_right_behind_what_they_read(group, pdl):
+    """Weights, x and the workspace are written by the work just before a call, and a
+    step's output is the next one's input: eager, and captured behind a copy and a
+    join with another stream."""
+    wl = Workload("f_chain", T=5, d=256, h=256, E=6, k=2, n_shared=1, h_shared=128)
+    inp = I.layer_inputs(wl)
+    cfg, g, W = device_weights(wl, inp)
+    if group:
+        sets = [M.quantize_weights(cfg, *W[:2], group),
+                M.quantize_weights(cfg, *W[2:], group, shared=True)]
+        W = [*sets[0], *sets[1]]
+    layers = [M.FewLayer(cfg, g["Wr"], None, *[torch.zeros_like(w) for w in W], group=group or None)
+              for _ in range(3)]
+    x = torch.zeros_like(g["x"])
+
+    def steps():
+        x.copy_(g["x"])
+        y = x
+        for layer in layers:
+            for own, w in zip(layer._held[2:], W):
+                own.copy_(w)
+            y = layer(y)["out"]
+        return y
+
+    def clear():
+        x.zero_()
+        for layer in layers:
+            layer.bufs["out"].zero_()
+            for own in layer._held[2:]:
+                own.zero_()
+            layer.ws.fill_(255)
+        torch.cuda.synchronize()
+
+    want = g["x"]
+    for layer in layers:  # one at a time
+        for own, w in zip(layer._held[2:], W):
+            own.copy_(w)
+        torch.cuda.synchronize()
+        want = run(layer, want)["out"].clone()
+    assert torch.isfinite(want.float()).all() and want.float().abs().max() > 0
+    M.moe_set_pdl(pdl)
+    try:
+        for _ in range(3):
+            clear()
+            got = steps()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+        s, side = torch.cuda.Stream(), torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            side.wait_stream(s)
+            with torch.cuda.stream(side):
+                for layer in layers:
+                    layer.bufs["routed"].zero_()
+            s.wait_stream(side)
+            got = steps()
+        for _ in range(3):
+            clear()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+        del graph
+    finally:
+        M.moe_set_pdl(True)
+
+
 def test_two_layers_on_two_streams():
     """Calls of layers with their own workspaces may overlap."""
     made_ = [(*made(n, q), q) for n, q in (("many", 0), ("full", 64))]
