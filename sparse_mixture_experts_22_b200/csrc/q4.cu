@@ -11,8 +11,12 @@
 // One pass, bound by memory.  A warp takes 16 rows x 128 columns: lane (half,
 // c) reads the eight weights 8c.. of row i (half 0) and row i + 8 (half 1) for i
 // = 0..7, so that a row's 256 bytes are one access and eight are in flight.  The
-// fragment order gathers a word from four lanes (two rows, two runs of eight
-// columns); the lanes exchange their eight codes as one word each.
+// two halves exchange one word of codes for each, which leaves every lane a word
+// in fragment order.  d = 4096, h = 14336, 8 experts,
+// group 128 (3.5 GB): packed to 4 bits in 603 us and back in 537, 5.9 and 6.6 TB/s.
+// What counts is bytes in flight: a tile a warp (a grid of 8 blocks an SM that steps
+// over the tiles took 693 and 623), eight rows' loads before the first is used (four:
+// 691), and four blocks of 64 registers an SM rather than three of 74 (743).
 #include "common.cuh"
 #include "few.h"
 #include "kernels.h"
@@ -29,67 +33,68 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
-// Codes of eight weights, nibble e = q of element e in two's complement.  q = rint(w
-// / s) without divisions or conversions: w inv + 1.5 2^23 leaves the nearest integer
-// in the low bits, and w inv is within 2^-19 of the quotient (the fast reciprocal is
-// off by 2 ulp).  As w and s have 8 significant bits and |w / s| <= 7.03 (so that
-// nothing clips), the quotient is either n + 1/2 exactly or at least 2^-10 away from
-// it; the exact remainder tells the half and sends it to the even code.
-__device__ __forceinline__ uint32_t codes_of(const float* w, float s) {
-    uint32_t out = 0;
+// w / s rounded to nearest even, in the low bits of the result: two additions, no
+// division or conversion.  w inv is within 2^-19 of the quotient (|w / s| <= 7.03, the
+// fast reciprocal is off by 2 ulp), and the first addition leaves it on a grid of
+// 2^-11: as w and s have 8 significant bits, the quotient is n + 1/2 exactly, which it
+// stays, or at least 2^-9 away from it, on the same side after.  The second rounds to
+// integers.
+__device__ __forceinline__ uint32_t code_of(float w, float inv) {
+    return __float_as_uint(fmaf(w, inv, 6144.f) + (12582912.f - 6144.f));
+}
+
+// The low bytes of four words as one.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Codes of eight weights in the low nibbles of eight bytes: columns 0..3 in x.
+__device__ __forceinline__ uint2 codes_of(const float* w, float s) {
+    uint32_t q[8];
     if (s >= 1.1754944e-38f && s <= 8.5070592e37f) {  // (the fast reciprocal's range)
-        const float inv = __fdividef(1.f, s), half = 0.5f * s;
+        const float inv = __fdividef(1.f, s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float t = fmaf(w[e], inv, 12582912.f);
-            const float rest = fmaf(12582912.f - t, s, w[e]);
-            uint32_t code = __float_as_uint(t);
-            if (fabsf(rest) == half && (code & 1)) code += rest > 0.f ? 1 : -1;
-            out |= (code & 15) << (4 * e);
-        }
+        for (int e = 0; e < 8; ++e) q[e] = code_of(w[e], inv);
     } else {  // no scale, or one at the end of the range
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float q = s > 0.f ? rintf(w[e] / s) : 0.f;
-            out |= (uint32_t)((int)fminf(fmaxf(q, -7.f), 7.f) & 15) << (4 * e);
-        }
+        for (int e = 0; e < 8; ++e)
+            q[e] = (uint32_t)(int)(s > 0.f ? fminf(fmaxf(rintf(w[e] / s), -7.f), 7.f) : 0.f);
     }
-    return out;
+    return make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
 }
 
-// Four nibbles (bits 0..15) to the low halves of four bytes, and back.
-__device__ __forceinline__ uint32_t spread(uint32_t n) {
-    n = (n | n << 8) & 0x00FF00FFu;
-    return (n | n << 4) & 0x0F0F0F0Fu;
-}
-__device__ __forceinline__ uint32_t gather(uint32_t b) {
-    b = (b | b >> 4) & 0x00FF00FFu;
-    return (b | b >> 8) & 0xFFFFu;
-}
-
-// The lanes' codes (lane (half, c): row g + 8 half, columns 8c..) as fragment
-// words: lane (t, s) = 8t + s gets the word of fragment lane 4g + t, 16-column
-// step s.
-__device__ __forceinline__ uint32_t to_fragment(uint32_t codes) {
-    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7, c = 2 * s + (t >> 1);
-    const uint32_t lo = __shfl_sync(0xffffffffu, codes, c) >> (16 * (t & 1));
-    const uint32_t hi = __shfl_sync(0xffffffffu, codes, 16 + c) >> (16 * (t & 1));
-    return spread(lo & 0xFFFFu) << 4 | spread(hi & 0xFFFFu);
+// A lane's codes (row g + 8 half, columns 8c..8c + 7) to a word in fragment order:
+// lane (half, c) gets that of fragment lane 4g + 2 (c & 1) + half, 16-column step c >> 1.
+__device__ __forceinline__ uint32_t to_fragment(uint2 codes, int half) {
+    const uint32_t mine = half ? codes.y : codes.x;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, half ? codes.x : codes.y, 16);
+    const uint32_t hi = half ? other : mine, lo = half ? mine : other;  // rows g, g + 8
+    return (hi << 4 & 0xF0F0F0F0u) | (lo & 0x0F0F0F0Fu);
 }
 
-// The other way: fragment words of lanes (t, s) to the eight codes of lane (half, c).
-__device__ __forceinline__ uint32_t from_fragment(uint32_t w) {
-    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
-    const uint32_t a = __shfl_sync(0xffffffffu, w, 16 * (c & 1) + (c >> 1));
-    const uint32_t b = __shfl_sync(0xffffffffu, w, 16 * (c & 1) + 8 + (c >> 1));
+// The other way; the nibbles' bytes come without their sign.
+__device__ __forceinline__ uint2 from_fragment(uint32_t w, int half) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 16);
     const int shift = half ? 0 : 4;
-    return gather(a >> shift & 0x0F0F0F0Fu) | gather(b >> shift & 0x0F0F0F0Fu) << 16;
+    const uint32_t mine = w >> shift & 0x0F0F0F0Fu, its = other >> shift & 0x0F0F0F0Fu;
+    return half ? make_uint2(its, mine) : make_uint2(mine, its);
+}
+
+// Codes of two neighbouring columns (bytes 2i, 2i + 1 of n) times s, in bf16: 128 + (q +
+// 8) as it lies, less 136, is q, and the product is rounded once.
+__device__ __forceinline__ uint32_t value_pair(uint32_t n, int i, __nv_bfloat162 s) {
+    const uint32_t b = __byte_perm(n ^ 0x08080808u, 0x43434343u, i ? 0x4342 : 0x4140);
+    __nv_bfloat162 v;
+    memcpy(&v, &b, 4);
+    v = __hmul2(__hsub2(v, __float2bfloat162_rn(136.f)), s);
+    uint32_t o;
+    memcpy(&o, &v, 4);
+    return o;
 }
 
 // 16 rows x 128 columns of bf16 weights at W (ld elements a row; row i and row
-// i + 8 begin at W + i ld and W + up + i ld) <-> codes and scales.  word(g):
-// where lane (t, s) keeps the word of fragment lane 4g + t; scale(q, r): the
-// scale of group q, row r.
+// i + 8 begin at W + i ld and W + up + i ld) <-> codes and scales.  word(g): where
+// this lane keeps its word of rows g, g + 8; scale(q, r): the scale of group q, row r.
 template <int G, bool QUANT, typename Word, typename Scale>
 __device__ __forceinline__ void block_pass(__nv_bfloat16* W, int64_t ld, int64_t up, Word word,
                                            Scale scale) {
@@ -108,42 +113,40 @@ __device__ __forceinline__ void block_pass(__nv_bfloat16* W, int64_t ld, int64_t
                 w[e] = __uint_as_float(e & 1 ? u[e / 2] & 0xFFFF0000u : u[e / 2] << 16);
                 m = fmaxf(m, fabsf(w[e]));
             }
-            const float s = bf16_round(group_max<G>(m) / 7.f);
+            // (m / 7 is never within 2^-12 of itself of a midpoint of bf16, so the
+            // product by the rounded 1 / 7 rounds to the same value)
+            const float s = bf16_round(group_max<G>(m) * (1.f / 7.f));
             if (c % (G / 8) == 0) *scale(c / (G / 8), g + 8 * half) = __float2bfloat16_rn(s);
-            *word(g) = to_fragment(codes_of(w, s));
+            *word(g) = to_fragment(codes_of(w, s), half);
         }
     } else {
         uint32_t words[8];
-        float s[8];
+        __nv_bfloat16 s[8];
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
             words[g] = *word(g);
-            s[g] = __bfloat162float(*scale(c / (G / 8), g + 8 * half));
+            s[g] = *scale(c / (G / 8), g + 8 * half);
         }
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-            const uint32_t codes = from_fragment(words[g]);
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = (float)((int)(codes << (28 - 4 * e)) >> 28) * s[g];
-            uint4 o;
-            o.x = pack_bf16x2(v[0], v[1]);
-            o.y = pack_bf16x2(v[2], v[3]);
-            o.z = pack_bf16x2(v[4], v[5]);
-            o.w = pack_bf16x2(v[6], v[7]);
-            *reinterpret_cast<uint4*>(row + g * ld) = o;
+            const uint2 n = from_fragment(words[g], half);
+            const __nv_bfloat162 ss = __bfloat162bfloat162(s[g]);
+            *reinterpret_cast<uint4*>(row + g * ld) =
+                make_uint4(value_pair(n.x, 0, ss), value_pair(n.x, 1, ss), value_pair(n.y, 0, ss),
+                           value_pair(n.y, 1, ss));
         }
     }
 }
 
-// One warp per tile of 16 rows x 128 columns of W13.
+// A set: one warp per 16 rows x 128 columns, first those of W13 (t13 tiles), then of W2p
+// (t2).
 template <int G, bool QUANT>
-__global__ void __launch_bounds__(256)
-    q13_kernel(__nv_bfloat16* W13, uint8_t* Q13, int64_t tiles, int hid, int d) {
-    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7;
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < tiles;
-         i += warps) {
+__global__ void __launch_bounds__(256, QUANT ? 4 : 5)
+    q4_kernel(__nv_bfloat16* W13, uint8_t* Q13, int64_t t13, __nv_bfloat16* W2p, uint32_t* Q2,
+              __nv_bfloat16* scales2, int64_t t2, int hid, int d) {
+    const int lane = threadIdx.x & 31, c = lane & 15, t = 2 * (c & 1) + (lane >> 4), s = c >> 1;
+    int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (i < t13) {
         const int64_t b = i >> 2;   // block of 32 hidden units x 128 columns
         const int tile = (int)(i & 3);
         const int kb = (int)(b % (d / 128));
@@ -156,22 +159,12 @@ __global__ void __launch_bounds__(256)
             W13 + gate * d + kb * 128, d, (int64_t)128 * d,
             [&](int g) { return codes + (4 * g + t) * 4; },
             [&](int q, int r) { return sc + q * 64 + r; });
-    }
-}
-
-// One warp per 16 rows x 128 hidden units of W2p.
-template <int G, bool QUANT>
-__global__ void __launch_bounds__(256)
-    q2_kernel(__nv_bfloat16* W2p, uint32_t* Q2, __nv_bfloat16* scales, int64_t tiles, int hid) {
-    const int lane = threadIdx.x & 31, t = lane >> 3, s = lane & 7;
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < tiles;
-         i += warps) {
+    } else if ((i -= t13) < t2) {
         const int kb = (int)(i % (hid / 128));
         const int64_t row = i / (hid / 128) * 16, rb = row / 128;  // over all experts' d rows
         const int tile = (int)(row % 128) / 16;
         uint32_t* codes = Q2 + ((rb * (hid / 32) + kb * 4 + (s >> 1)) * 8 + tile) * 64 + (s & 1);
-        __nv_bfloat16* sc = scales + (rb * (hid / G) + kb * (128 / G)) * 128 + tile * 16;
+        __nv_bfloat16* sc = scales2 + (rb * (hid / G) + kb * (128 / G)) * 128 + tile * 16;
         block_pass<G, QUANT>(
             W2p + row * hid + kb * 128, hid, (int64_t)8 * hid,
             [&](int g) { return codes + (4 * g + t) * 2; },
@@ -182,18 +175,13 @@ __global__ void __launch_bounds__(256)
 template <int G, bool QUANT>
 int launch_q4(const void* W13, const void* W2p, const void* Q13, const void* Q2, int n, int hid,
               int d, cudaStream_t st) {
-    auto grid = [](int64_t tiles) { return (int)((tiles + 7) / 8 < 1184 ? (tiles + 7) / 8 : 1184); };
     uint8_t* q2 = reinterpret_cast<uint8_t*>(const_cast<void*>(Q2));
-    const int64_t t13 = (int64_t)n * (hid / 8) * (d / 128);
-    q13_kernel<G, QUANT><<<grid(t13), 256, 0, st>>>(
+    const int64_t t13 = (int64_t)n * (hid / 8) * (d / 128), t2 = (int64_t)n * (d / 16) * (hid / 128);
+    q4_kernel<G, QUANT><<<(unsigned)((t13 + t2 + 7) / 8), 256, 0, st>>>(
         reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(W13)),
-        reinterpret_cast<uint8_t*>(const_cast<void*>(Q13)), t13, hid, d);
-    note_launch();
-    if (launch_result() != 0) return -1;
-    const int64_t t2 = (int64_t)n * (d / 16) * (hid / 128);
-    q2_kernel<G, QUANT><<<grid(t2), 256, 0, st>>>(
+        reinterpret_cast<uint8_t*>(const_cast<void*>(Q13)), t13,
         reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(W2p)), reinterpret_cast<uint32_t*>(q2),
-        reinterpret_cast<__nv_bfloat16*>(q2 + q2_code_bytes(n, hid, d)), t2, hid);
+        reinterpret_cast<__nv_bfloat16*>(q2 + q2_code_bytes(n, hid, d)), t2, hid, d);
     note_launch();
     return launch_result();
 }
