@@ -1750,7 +1750,7 @@ static_assert(MOE_FEW_MAX_T == FEW_MAX_T, "token limits differ");
 // Workspace of the few-token layer.
 struct FewPlan {
     Plan P;
-    size_t off_logits, off_table, off_xh, off_xf, off_ppart, off_hpart, off_cnt, off_idx, off_gate,
+    size_t off_logits, off_table, off_xq, off_xf, off_ppart, off_hpart, off_cnt, off_idx, off_gate,
         off_sums, off_part, total;
 };
 
@@ -1769,7 +1769,7 @@ static int few_plan_or_fail(const moe_config* cfg, FewPlan* f) {
     const size_t T = (size_t)P.T, E = (size_t)P.E, k = (size_t)P.k;
     f->off_logits = take(T * E * 4);
     f->off_table = take(T * (k + 1) * sizeof(int4));
-    f->off_xh = take(T * 2 * (size_t)P.d);
+    f->off_xq = take(T * 3 * (size_t)P.d);
     f->off_xf = take(T * 4);
     f->off_ppart = take(E * 4);
     f->off_hpart = take(4);
@@ -1849,7 +1849,7 @@ static int few_forward(const moe_config* cfg, int32_t group, const void* x, cons
     FewArgs a;
     memset(&a, 0, sizeof a);
     a.x = x;
-    a.xh = at<void>(ws, F.off_xh);
+    a.xq = at<int8_t>(ws, F.off_xq);
     a.xf = at<float>(ws, F.off_xf);
     a.logits = at<float>(ws, F.off_logits);
     a.bias = cfg->has_bias ? bias : nullptr;

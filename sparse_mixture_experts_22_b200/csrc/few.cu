@@ -9,7 +9,6 @@
 // the routing.  What a part adds to a token's output goes to a row of its own
 // in the workspace; the combine adds a token's rows in a fixed order, so the
 // result does not depend on which CTA finished first.
-#include <cuda_fp16.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -303,22 +302,29 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The same with f16 operands.
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
+// c (16 x 8, int32) += a (16 x 32) b (32 x 8), signed 8-bit
+__device__ __forceinline__ void imma(int (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                     uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
         " {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr float CODE_ONE = 16777216.f;  // 1 / the value of a code of 1 in a fragment
+// Two code words (32 columns) as an A fragment of values 16 q.
+__device__ __forceinline__ void codes_to_frag(uint32_t w0, uint32_t w1, uint32_t (&f)[4]) {
+    constexpr uint32_t M = 0xF0F0F0F0u;
+    f[0] = w0 & M;
+    f[1] = (w0 << 4) & M;
+    f[2] = w1 & M;
+    f[3] = (w1 << 4) & M;
+}
 
-// A word of codes as an f16 A fragment of values q 2^-24.
-__device__ __forceinline__ void codes_to_frag(uint32_t w, uint32_t (&f)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = __funnelshift_r(w, w, 4 * i) & 0x80078007u;
+// An integer of magnitude below 2^22 to fp32 (an addition instead of the slower
+// conversion): a group's sum is at most 128 * 112 * 128 = 1.84 million.
+__device__ __forceinline__ float small_int(int v) {
+    return __int_as_float(v + 0x4B400000) - 12582912.f;
 }
 
 __device__ __forceinline__ float lds_bf16(uint32_t addr) {
@@ -346,27 +352,29 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 //
 // bf16 weights: m16n8k16 products with fp32 sums, H as two bf16 parts.
 //
-// 4-bit weights: m16n8k16 products of f16.  A code's magnitude is an f16 as it lies (a
-// subnormal: m 2^-24), so a fragment costs a rotation and a mask for two codes.  As bf16
-// fragments the codes took shifts, masks and subtractions; as 8-bit integers they need x
-// in three planes of digits, columns that fill three of the integer products' tiles at 8
-// tokens where f16 fills one (clocks per 2048 weights and scheduler, of which HBM takes
-// 184 to bring them: int8 74 with one tile, 161 with three, 296 with six; f16 93 with
-// one, 174 with two).  A row of x is brought into f16's range by a power of two of its
-// own, which leaves every bf16 exact down to 2^-29 of the row's largest magnitude and
-// within 2^-39 of that below; H likewise per expert and part, as two f16 parts (22
-// bits).  Sums of a group are in fp32, and the group's scale multiplies them in fp32.
+// 4-bit weights: the products are exact.  A row of x is an integer of 23 bits
+// times a power of two (of the row's largest magnitude: the rounding is 2^-22 of
+// that at most, what an fp32 sum of the row loses too), held as three planes of
+// signed 8-bit digits; H likewise per expert and part.  The planes are columns of
+// one 8-bit product, which takes the codes after two masks and a shift per 8
+// codes -- as bf16 fragments they took three shifts, four masks and four
+// subtractions, and 30 clocks per 256 weights and scheduler against 11, where HBM
+// brings 256 in 23.  Sums within a group are exact in int32; a group's scale
+// multiplies its sum in fp32.  A tile of 8 columns holds the planes of two
+// tokens, two tiles those of five, three those of eight.
 //
 // Copied bf16 tiles are swizzled and token rows pitched by an odd multiple of 16
 // bytes, so that ldmatrix meets no bank twice; codes arrive in fragment order and
 // are read as they lie.
-template <int G>   // group (0: bf16)
+template <int G, int TT>   // group (0: bf16), most tokens
 struct Shape {
     static constexpr bool Q4 = G > 0;
     static constexpr int GG = Q4 ? G : 128;
     static constexpr int KW = 4;                           // warps along the columns
     static constexpr int KB = Q4 ? 128 : 64;               // least columns of a warp in a stage
     static constexpr int QB = q13_block_bytes(GG);
+    static constexpr int XROWS = Q4 ? 3 : 1;               // rows of a stage per token
+    static constexpr int XBYTES = Q4 ? 1 : 2;              // bytes of an element
     // a stage of the second half: 2 blocks of 128 rows x panels of 32 units, with 4
     // bits then the scales of the groups they meet (one more than they fill, unless a
     // group is a panel)
@@ -377,12 +385,12 @@ struct Shape {
     static __device__ __forceinline__ int down(int panels) {
         return 2 * panels * PANEL + (Q4 ? 2 * groups(panels) * 256 : 0);
     }
-    // H.  bf16: all tokens' high, then all low parts.  4 bits: a row of a token is first
-    // fp32, then its high and, HPART bytes on, its low parts (rows of 8 tokens, or both
-    // parts of 4, meet no bank twice)
-    static constexpr int HPART = FEW_HCAP * 2 + 64;
-    static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 144 : (FEW_HCAP + 8) * 2;
-    static_assert(!Q4 || HPART + FEW_HCAP * 2 <= HPITCH, "the parts fit the row they replace");
+    // H: bf16 high, then low parts of the tokens' rows; 4 bits: a row first fp32, then
+    // its three planes HPLANE bytes apart (33 and 131 times 16 bytes: rows of
+    // consecutive (token, plane) meet no bank twice)
+    static constexpr int HPLANE = FEW_HCAP + 16;
+    static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 48 : (FEW_HCAP + 8) * 2;
+    static_assert(!Q4 || 3 * HPLANE <= HPITCH, "the planes fit the row they replace");
 };
 
 // Shared memory of one call: the ring, H and the warps' sums are sized by the most
@@ -419,9 +427,9 @@ __device__ __forceinline__ Geometry geometry(int tokens, int bytes) {
         g.blocks = blocks;
         g.panels = S::Q4 ? 8 : 2;
         g.ka = S::KW * S::KB * blocks;
-        g.xpitch = g.ka * 2 + 16;
+        g.xpitch = g.ka * S::XBYTES + 16;
         g.xoff = S::Q4 ? g.ka / 128 * S::QB : g.ka * 128;
-        const int up = g.xoff + tokens * g.xpitch;
+        const int up = g.xoff + tokens * S::XROWS * g.xpitch;
         g.slot = (max(up, S::down(g.panels)) + 1023) / 1024 * 1024;
         g.stages = min(ring / g.slot, MAX_STAGES);
         if (g.stages >= 3) break;
@@ -519,11 +527,11 @@ struct Bringer {
 // The weights' copies, stage by stage: per part the first half (experts, granules,
 // columns), then the second (experts, 256 rows of d, panels).  False when a wait
 // ran out.
-template <int G>
+template <int G, int TT>
 __device__ __forceinline__ bool bring_weights(const FewArgs& a, const Routing& r,
                                               const FewMaps& maps, Seg* segs, Bringer c,
                                               int32_t* issued) {
-    using S = Shape<G>;
+    using S = Shape<G, TT>;
     const int lane = threadIdx.x & 31;
     const int d = a.d;
     const uint64_t once = l2_policy_evict_first();
@@ -615,34 +623,38 @@ __device__ __forceinline__ bool bring_weights(const FewArgs& a, const Routing& r
     return true;
 }
 
-// The token rows of the first half (x, or its f16 form), 16 bytes a lane, by warp
+// The token rows of the first half (x, or its planes), 16 bytes a lane, by warp
 // `share` of TOKEN_WARPS; every lane arrives on every stage, when its copies have
 // landed.
-template <int G>
+template <int G, int TT>
 __device__ __forceinline__ bool bring_tokens(const FewArgs& a, const Routing& r, Seg* segs,
                                              Bringer c, int share) {
-    const int rowbytes = c.geo.ka * 2;  // of a stage: a copy of every lane or more
+    using S = Shape<G, TT>;
+    const int rowbytes = c.geo.ka * S::XBYTES;  // of a stage: one copy of every lane, or two
     const int lane = threadIdx.x & 31;
-    const int pitch = a.d * 2;  // bytes of a row in memory
-    const uint8_t* x = reinterpret_cast<const uint8_t*>(G ? a.xh : a.x) + lane * 16;
+    const int pitch = a.d * S::XBYTES;  // bytes of a row in memory
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(S::Q4 ? (const void*)a.xq : a.x) + lane * 16;
     for (int v = blockIdx.x; v < r.V; v += gridDim.x) {
         const int nseg = segments(a, r, v, segs);
         for (int i = 0; i < nseg; ++i) {
             const Seg s = segs[i];
+            const int rows = s.n * S::XROWS;
             // lane q keeps where this warp's q-th row begins
             const int mine = share + TOKEN_WARPS * lane;
-            const int64_t at = mine < s.n ? (int64_t)r.tok[s.item][mine] * pitch : 0;
+            const int64_t at = mine < rows ? ((int64_t)r.tok[s.item][mine / S::XROWS] * S::XROWS +
+                                              mine % S::XROWS) * pitch
+                                           : 0;
             for (int j = 0; j < s.len; j += FEW_GRAN)
                 for (int k0 = 0; k0 < pitch; k0 += rowbytes) {
                     if (!c.open()) return false;
                     const uint32_t dst = c.at() + c.geo.xoff + lane * 16;
-                    const int bytes = min(rowbytes, pitch - k0) - lane * 16;
-                    for (int q = 0, row = share; row < s.n; ++q, row += TOKEN_WARPS) {
-                        const uint8_t* src = x + __shfl_sync(0xffffffffu, at, q) + k0;
+                    for (int q = 0, row = share; row < rows; ++q, row += TOKEN_WARPS) {
+                        const int64_t from = __shfl_sync(0xffffffffu, at, q);
+                        const uint8_t* src = x + from + k0;
                         const uint32_t to = dst + row * c.geo.xpitch;
-#pragma unroll
-                        for (int o = 0; o < (G ? 2048 : 512); o += 512)
-                            if (o < bytes) cp_async16(to + o, src + o);
+                        if (k0 + lane * 16 < pitch) cp_async16(to, src);
+                        if (rowbytes > 512 && k0 + 512 + lane * 16 < pitch)
+                            cp_async16(to + 512, src + 512);
                     }
                     cp_async_arrive(c.bar());
                     c.p.next();
@@ -692,7 +704,7 @@ struct Consumer {
 // tokens.  red: where they go, [NT][8 tokens][20] floats.
 template <int TT>
 __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float* red) {
-    using S = Shape<0>;
+    using S = Shape<0, TT>;
     constexpr int NT = (TT + 7) / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
     const int lm = lane & 7, lq = lane >> 3;         // row and matrix of an ldmatrix address
@@ -742,60 +754,92 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
     }
 }
 
-// The same for 4 bits.
-template <int G, int NT>
+// Column c of the 4-bit products is token c / 3, plane c % 3: n tokens take 3 n / 8
+// tiles of 8 columns, rounded up.
+// Planes joined: v[tile][4] as the products leave them to y[4], the sums of
+// tokens 2 ft and 2 ft + 1 in the lane's two rows, as a tile of 8 tokens would
+// leave them.  A lane's tokens are columns 6 ft .. 6 ft + 5, in three lanes of a
+// quad; in each round every lane gives one pair of columns and takes one.
+template <int TILES>
+__device__ __forceinline__ void join_planes(const float (*v)[4], float (&y)[4]) {
+    const int ft = threadIdx.x & 3;
+    float pair[3][4];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        // pair i of lane ft is pair 3 ft + i of the group: tile (3 ft + i) / 4, lane (3 ft
+        // + i) % 4; seen from the giving lane, the tile is
+        int tile = 0;
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+            if ((4 * t + ft - i + 12) % 3 == 0 && 4 * t + ft >= i && (4 * t + ft - i) / 3 < 4) tile = t;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float give = v[0][q];
+#pragma unroll
+            for (int t = 1; t < TILES; ++t) give = tile == t ? v[t][q] : give;
+            if (tile >= TILES) give = 0.f;
+            pair[i][q] = __shfl_sync(0xffffffffu, give, (threadIdx.x & 28) | ((3 * ft + i) & 3));
+        }
+    }
+#pragma unroll
+    for (int hi = 0; hi < 2; ++hi) {
+        y[2 * hi] = fmaf(pair[1][2 * hi], 65536.f, fmaf(pair[0][2 * hi + 1], 256.f, pair[0][2 * hi]));
+        y[2 * hi + 1] =
+            fmaf(pair[2][2 * hi + 1], 65536.f, fmaf(pair[2][2 * hi], 256.f, pair[1][2 * hi + 1]));
+    }
+}
+
+// The same for 4 bits; TILES: tiles of 8 columns, up to three all computed, so that
+// their products overlap.
+template <int G, int TT, int TILES>
 __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* red) {
-    using S = Shape<G>;
-    constexpr int CH = NT == 1 ? 2 : 1;  // chains of products a tile, so that two always overlap
+    using S = Shape<G, TT>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
     const int lm = lane & 7, lq = lane >> 3;
-    uint32_t xrow[NT];
-    float acc[NT][4];
+    uint32_t xrow[TILES];
+    float acc[TILES][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        xrow[nt] = c.geo.xoff + min(nt * 8 + lm, s.n - 1) * c.geo.xpitch + kw * c.geo.blocks * 256 +
-                   lq * 16;
+    for (int t = 0; t < TILES; ++t) {
+        const int row = min(t * 8 + lm, 3 * s.n - 1);
+        xrow[t] = c.geo.xoff + row * c.geo.xpitch + kw * c.geo.blocks * 128 + lq * 16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[nt][q] = 0.f;
+        for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
     }
     auto block = [&](const uint8_t* stp, int kb) {
         const int blk = kw * c.geo.blocks + kb;
         const uint4* cw = reinterpret_cast<const uint4*>(stp + blk * S::QB + gw * 1024);
         const uint32_t st = smem_addr(stp);
-        const uint4 lo = cw[lane], hi = cw[32 + lane];
-        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        uint32_t f[4][4];
+        {
+            const uint4 lo = cw[lane], hi = cw[32 + lane];
+            codes_to_frag(lo.x, lo.y, f[0]);
+            codes_to_frag(lo.z, lo.w, f[1]);
+            codes_to_frag(hi.x, hi.y, f[2]);
+            codes_to_frag(hi.z, hi.w, f[3]);
+        }
         const uint32_t sa = st + blk * S::QB + 4096 + (gw * 16 + (lane >> 2)) * 2;
-        float g[NT][CH][4];
+        float sl[128 / S::GG], sh[128 / S::GG];
 #pragma unroll
-        for (int u = 0; u < 8; u += 2) {  // 32 columns
-            if (u * 16 % S::GG == 0)
+        for (int q = 0; q < 128 / S::GG; ++q) {
+            sl[q] = lds_bf16(sa + q * 128);
+            sh[q] = lds_bf16(sa + q * 128 + 16);
+        }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+        for (int t = 0; t < TILES; ++t) {
+            if (TILES > 3 && t * 8 >= 3 * s.n) break;
+            uint32_t b[2][4];
+            ldmatrix4(st + xrow[t] + kb * 128, b[0]);
+            ldmatrix4(st + xrow[t] + kb * 128 + 64, b[1]);
 #pragma unroll
-                    for (int q = 0; q < CH * 4; ++q) g[nt][q >> 2][q & 3] = 0.f;
-            uint32_t b[NT][4];
+            for (int q = 0; q < 128 / S::GG; ++q) {
+                int g[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) ldmatrix4(st + xrow[nt] + kb * 256 + u * 32, b[nt]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t f[4];
-                codes_to_frag(w[u + i], f);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_f16(g[nt][i % CH], f, b[nt][2 * i], b[nt][2 * i + 1]);
-            }
-            if ((u + 2) * 16 % S::GG == 0) {
-                const int q = u * 16 / S::GG;
-                const float sl = lds_bf16(sa + q * 128), sh = lds_bf16(sa + q * 128 + 16);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        acc[nt][0] = fmaf(g[nt][i][0], sl, acc[nt][0]);
-                        acc[nt][1] = fmaf(g[nt][i][1], sl, acc[nt][1]);
-                        acc[nt][2] = fmaf(g[nt][i][2], sh, acc[nt][2]);
-                        acc[nt][3] = fmaf(g[nt][i][3], sh, acc[nt][3]);
-                    }
+                for (int u = q * (S::GG / 32); u < (q + 1) * (S::GG / 32); ++u)
+                    imma(g, f[u], b[u / 2][2 * (u & 1)], b[u / 2][2 * (u & 1) + 1]);
+                acc[t][0] = fmaf(small_int(g[0]), sl[q], acc[t][0]);
+                acc[t][1] = fmaf(small_int(g[1]), sl[q], acc[t][1]);
+                acc[t][2] = fmaf(small_int(g[2]), sh[q], acc[t][2]);
+                acc[t][3] = fmaf(small_int(g[3]), sh[q], acc[t][3]);
             }
         }
     };
@@ -811,12 +855,14 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
         c.done();
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < (TILES + 2) / 3; ++nt) {
+        float y[4];
+        join_planes<(TILES < 3 ? TILES : 3)>(acc + 3 * nt, y);
         float* q = red + nt * 160 + 2 * (lane & 3) * 20 + (lane >> 2);
-        q[0] = acc[nt][0];
-        q[20] = acc[nt][1];
-        q[8] = acc[nt][2];
-        q[28] = acc[nt][3];
+        q[0] = y[0];
+        q[20] = y[1];
+        q[8] = y[2];
+        q[28] = y[3];
     }
 }
 
@@ -825,7 +871,7 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
 template <int TT>
 __device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool mine, uint32_t hs,
                                           float* out) {
-    using S = Shape<0>;
+    using S = Shape<0, TT>;
     constexpr int NT = (TT + 7) / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
     const int lm = lane & 7, lq = lane >> 3;
@@ -885,24 +931,22 @@ __device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool
     }
 }
 
-// The same for 4 bits.  hf: what a token's products are multiplied by.  A tile of 8
-// columns holds 8 tokens, high and low parts by turns, or (PAIR) both parts of 4.
-template <int G, int NT, bool PAIR>
+// The same for 4 bits.  hf: what the planes of H are multiplied by, per token.
+template <int G, int TT, int TILES>
 __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool mine, uint32_t hs,
                                         const float* hf, float* out) {
-    using S = Shape<G>;
+    using S = Shape<G, TT>;
     constexpr int PG = S::GG / 32;  // panels of a group
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
     const int lm = lane & 7, lq = lane >> 3, ft = lane & 3;
-    uint32_t hrow[NT];
-    float acc[NT][4];
+    uint32_t hrow[TILES];
+    float acc[TILES][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        hrow[nt] = hs + s.hb * 2 +
-                   (PAIR ? min(lm >> 1, s.n - 1) * S::HPITCH + (lm & 1) * S::HPART + lq * 16
-                         : min(nt * 8 + lm, s.n - 1) * S::HPITCH + (lq >> 1) * S::HPART + (lq & 1) * 16);
+    for (int t = 0; t < TILES; ++t) {
+        const int row = min(t * 8 + lm, 3 * s.n - 1);
+        hrow[t] = hs + row / 3 * S::HPITCH + row % 3 * S::HPLANE + s.hb + lq * 16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[nt][q] = 0.f;
+        for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
     }
     const int step = s.step(c.geo.panels);
     for (int p0 = 0; p0 < s.len / 32; p0 += step) {
@@ -914,45 +958,36 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
             const uint2* cw = reinterpret_cast<const uint2*>(stp + rb * block + tile * 256) + lane;
             const uint32_t sa = smem_addr(stp) + 2 * block + rb * scale +
                                 (tile * 16 + (lane >> 2)) * 2;
-            // the panels of one group at a time
+            // the panels of one group at a time: their sum is exact
             for (int p = 0; p < np;) {
                 const int gq = (first + p) / PG - q0;
                 const int pe = min(np, (q0 + gq + 1) * PG - first);
                 const float sl = lds_bf16(sa + gq * 256), sh = lds_bf16(sa + gq * 256 + 16);
-                float g[NT][2][4];
+                uint32_t f[PG][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) g[nt][q >> 2][q & 3] = 0.f;
-#pragma unroll
-                for (int i = 0; i < PG; ++i) {
-                    if (p + i >= pe) break;
-                    const uint2 w = cw[(p + i) * 256];
-                    uint32_t f[2][4], b[4];
-                    codes_to_frag(w.x, f[0]);
-                    codes_to_frag(w.y, f[1]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t at = hrow[nt] + (p0 + p + i) * 64;
-                        ldmatrix4(at, b);
-                        mma_f16(g[nt][0], f[0], b[0], b[1]);
-                        mma_f16(g[nt][1], f[PAIR], b[2], b[3]);
-                        if (!PAIR) {
-                            ldmatrix4(at + 32, b);
-                            mma_f16(g[nt][0], f[1], b[0], b[1]);
-                            mma_f16(g[nt][1], f[1], b[2], b[3]);
-                        }
-                    }
+                for (int i = 0; i < PG; ++i) {  // (a panel past the group: zero codes)
+                    const uint2 w = p + i < pe ? cw[(p + i) * 256] : make_uint2(0, 0);
+                    codes_to_frag(w.x, w.y, f[i]);
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int t = 0; t < TILES; ++t) {
+                    if (TILES > 3 && t * 8 >= 3 * s.n) break;
+                    int g[2][4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        acc[nt][0] = fmaf(g[nt][i][0], sl, acc[nt][0]);
-                        acc[nt][1] = fmaf(g[nt][i][1], sl, acc[nt][1]);
-                        acc[nt][2] = fmaf(g[nt][i][2], sh, acc[nt][2]);
-                        acc[nt][3] = fmaf(g[nt][i][3], sh, acc[nt][3]);
+                    for (int q = 0; q < 4; ++q) g[0][q] = g[1][q] = 0;
+#pragma unroll
+                    for (int i = 0; i < PG; i += 2) {  // an H fragment serves two panels
+                        uint32_t b[4];
+                        // (and its second half of the group may lie past the share)
+                        ldmatrix4(hrow[t] + (p0 + (p + i < pe ? p + i : p)) * 32, b);
+                        imma(g[0], f[i], b[0], b[1]);
+                        if (PG > 1) imma(g[1], f[(i + 1) % PG], b[2], b[3]);
                     }
+                    acc[t][0] = fmaf(small_int(g[0][0] + g[1][0]), sl, acc[t][0]);
+                    acc[t][1] = fmaf(small_int(g[0][1] + g[1][1]), sl, acc[t][1]);
+                    acc[t][2] = fmaf(small_int(g[0][2] + g[1][2]), sh, acc[t][2]);
+                    acc[t][3] = fmaf(small_int(g[0][3] + g[1][3]), sh, acc[t][3]);
+                }
                 p = pe;
             }
         }
@@ -960,40 +995,39 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
     }
     if (!mine) return;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int n = PAIR ? ft : nt * 8 + 2 * ft;
+    for (int nt = 0; nt < (TILES + 2) / 3; ++nt) {
+        float y[4];
+        join_planes<(TILES < 3 ? TILES : 3)>(acc + 3 * nt, y);
+        const int n = nt * 8 + 2 * ft;
         float* q = out + (int64_t)n * d;
-        if (PAIR) {
-            if (n < s.n) {
-                q[0] = (acc[nt][0] + acc[nt][1]) * CODE_ONE * hf[n];
-                q[8] = (acc[nt][2] + acc[nt][3]) * CODE_ONE * hf[n];
-            }
-        } else {
-            if (n < s.n) {
-                q[0] = acc[nt][0] * CODE_ONE * hf[n];
-                q[8] = acc[nt][2] * CODE_ONE * hf[n];
-            }
-            if (n + 1 < s.n) {
-                q[d] = acc[nt][1] * CODE_ONE * hf[n + 1];
-                q[d + 8] = acc[nt][3] * CODE_ONE * hf[n + 1];
-            }
+        if (n < s.n) {
+            q[0] = y[0] * hf[n];
+            q[8] = y[2] * hf[n];
+        }
+        if (n + 1 < s.n) {
+            q[d] = y[1] * hf[n + 1];
+            q[d + 8] = y[3] * hf[n + 1];
         }
     }
 }
 
-// Exponent e that brings magnitudes up to m (finite) to [2^14, 2^15), f16's upper end; 2^-e
-// is an fp32, so that the smallest rows end lower.
-__device__ __forceinline__ int f16_exponent(float m) { return m > 0.f ? min(14 - ilogbf(m), 140) : 0; }
+// v 2^e as three signed digits of 8 bits, low first (|v 2^e| < 2^22).
+__device__ __forceinline__ void digits(float scaled, int8_t (&p)[3]) {
+    int v = __float2int_rn(scaled);
+    p[0] = (int8_t)v;
+    v = (v - p[0]) >> 8;
+    p[1] = (int8_t)v;
+    p[2] = (int8_t)((v - p[1]) >> 8);
+}
 
-// Where column c of 16 lies in rows of x and H for 4 bits: lane t's codes are those of
-// columns 4t .. 4t + 3, and the product's fragments take places 2t, 2t + 1, 2t + 8, 2t + 9.
-__device__ __forceinline__ int f16_place(int c) { return (c >> 2) * 2 + (c & 1) + (c & 2) * 4; }
+// Exponent e that brings magnitudes up to m (finite) below 2^22.
+__device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? 21 - ilogbf(m) : 0; }
 
 template <int G, int TT>
 __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring,
                         const Geometry& geo, uint64_t* full, uint64_t* empty, uint8_t* Hs,
                         float* red, float (*hf)[FT], int32_t* flags) {
-    using S = Shape<G>;
+    using S = Shape<G, TT>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gw = warp >> 2, gt = tid & 127;  // group of four warps; thread of the group
     const int d = a.d;
@@ -1026,10 +1060,14 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                 float* mine = base + warp * (geo.nt * 160);
                 if constexpr (!S::Q4)
                     up_bf16<TT>(c, s, d, mine);
+                else if (TT <= 2 || s.n <= 2)
+                    up_q4<G, TT, 1>(c, s, d, mine);
+                else if (s.n <= 5)
+                    up_q4<G, TT, TT <= 2 ? 1 : 2>(c, s, d, mine);
                 else if (TT <= 8 || s.n <= 8)
-                    up_q4<G, 1>(c, s, d, mine);
+                    up_q4<G, TT, TT <= 2 ? 1 : 3>(c, s, d, mine);
                 else
-                    up_q4<G, 2>(c, s, d, mine);
+                    up_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 3 : 6>(c, s, d, mine);
                 named_sync(2 + gw, 128);
                 if (n < s.n) {
                     float ga = 0.f, up = 0.f;
@@ -1041,11 +1079,7 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                         up += q[8];
                     }
                     const int at = s.hb + j + gw * 8 + jj;
-                    if (S::Q4) {
-                        ga = ga * CODE_ONE * xf;
-                        up = up * CODE_ONE * xf;
-                    }
-                    const float hv = silu_f(ga) * up * gate;
+                    const float hv = silu_f(ga * xf) * (up * xf) * gate;
                     if (S::Q4) {
                         reinterpret_cast<float*>(Hs + n * S::HPITCH)[at] = hv;
                     } else {
@@ -1059,15 +1093,13 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
         }
         named_sync(1, CONSUMERS);
         if constexpr (S::Q4) {
-            // a warp turns a token's row into its two parts, in place
+            // a warp turns a token's row into planes, in place
             if (warp < r.most) {
                 const float* row = reinterpret_cast<const float*>(Hs + warp * S::HPITCH);
                 float h[FEW_HCAP / 32];
 #pragma unroll
                 for (int q = 0; q < FEW_HCAP / 32; ++q) h[q] = row[q * 32 + lane];
                 __syncwarp();
-                __half* dst = reinterpret_cast<__half*>(Hs + warp * S::HPITCH) + (lane & 16) +
-                              f16_place(lane & 15);
                 for (int i = 0; i < nseg; ++i) {
                     const Seg& s = segs[i];
                     if (warp >= s.n) continue;
@@ -1083,16 +1115,17 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                     odd = __any_sync(0xffffffffu, odd);
-                    const int e = odd ? 0 : f16_exponent(m);
+                    const int e = odd ? 0 : plane_exponent(m);
+                    int8_t* dst = reinterpret_cast<int8_t*>(Hs + warp * S::HPITCH) + lane;
 #pragma unroll
                     for (int q = 0; q < FEW_HCAP / 32; ++q)
                         if (q >= p0 && q < p1) {
-                            const float v = odd ? 0.f : scalbnf(h[q], e);
-                            const __half hi = __float2half_rn(v);
-                            dst[q * 32] = hi;
-                            dst[S::HPART / 2 + q * 32] = __float2half_rn(v - __half2float(hi));
+                            int8_t pl[3];
+                            digits(odd ? 0.f : scalbnf(h[q], e), pl);
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) dst[k * S::HPLANE + q * 32] = pl[k];
                         }
-                    if (lane == 0) hf[i][warp] = odd ? NAN : scalbnf(1.f, -e);
+                    if (lane == 0) hf[i][warp] = odd ? NAN : scalbnf(0.0625f, -e);
                 }
             }
             named_sync(1, CONSUMERS);
@@ -1107,12 +1140,14 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                 const bool mine = r0 + rb * 128 < d;
                 if constexpr (!S::Q4)
                     down_bf16<TT>(c, s, d, mine, hs, out);
-                else if (s.n <= 4)
-                    down_q4<G, 1, true>(c, s, d, mine, hs, hf[i], out);
+                else if (TT <= 2 || s.n <= 2)
+                    down_q4<G, TT, 1>(c, s, d, mine, hs, hf[i], out);
+                else if (s.n <= 5)
+                    down_q4<G, TT, TT <= 2 ? 1 : 2>(c, s, d, mine, hs, hf[i], out);
                 else if (TT <= 8 || s.n <= 8)
-                    down_q4<G, 1, false>(c, s, d, mine, hs, hf[i], out);
+                    down_q4<G, TT, TT <= 2 ? 1 : 3>(c, s, d, mine, hs, hf[i], out);
                 else
-                    down_q4<G, 2, false>(c, s, d, mine, hs, hf[i], out);
+                    down_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 3 : 6>(c, s, d, mine, hs, hf[i], out);
             }
         }
     }
@@ -1122,7 +1157,7 @@ template <int G, int TT>
 __global__ void __launch_bounds__(FFN_THREADS, 1)
     few_ffn_kernel(const __grid_constant__ FewMaps maps, const __grid_constant__ FewArgs a,
                    int bytes) {
-    using S = Shape<G>;
+    using S = Shape<G, TT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = smem_raw + (-smem_addr(smem_raw) & 1023);
     Routing& r = *reinterpret_cast<Routing*>(ring + bytes);
@@ -1150,7 +1185,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     }
     pdl_trigger();
     __syncthreads();
-    pdl_wait();  // the router's logits (and f16 rows)
+    pdl_wait();  // the router's logits (and planes)
     route_batch(a, r);
     const Geometry geo = geometry<S>(r.most, bytes);
     if (warp < CONSUMERS / 32) {
@@ -1166,8 +1201,8 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         c.geo = geo;
         c.p.stages = geo.stages;
         const int w = warp - CONSUMERS / 32;
-        const bool ok = w == 0 ? bring_weights<G>(a, r, maps, segs[1], c, &flags[1])
-                               : bring_tokens<G>(a, r, segs[1 + w], c, w - 1);
+        const bool ok = w == 0 ? bring_weights<G, TT>(a, r, maps, segs[1], c, &flags[1])
+                               : bring_tokens<G, TT>(a, r, segs[1 + w], c, w - 1);
         if (!ok && (tid & 31) == 0) report_timeout(a.status);
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -1236,8 +1271,8 @@ __global__ void __launch_bounds__(CB_GROUPS * 8, 16)
 // eighth of d; the blocks' sums meet in the first one through its cluster's
 // shared memory, in block order.  W_r is read once whatever T, and even E = 8
 // spreads over 8 SMs, where one block per token took the latency of reading
-// the whole of W_r in turn.  With 4-bit weights one more cluster brings x into
-// f16's range (see the expert kernel).
+// the whole of W_r in turn.  With 4-bit weights one more cluster turns x into
+// planes (see the expert kernel).
 constexpr int RC = 8;
 constexpr int ROUTER_THREADS = 256;
 
@@ -1247,9 +1282,9 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
     return v;
 }
 
-// This block's eighth of every token's row as f16 times a power of two; xf[t] undoes
-// that.  Rows with an infinity or NaN get zeros and the factor NaN.
-__device__ void rows_to_f16(const FewArgs& a) {
+// Planes of this block's eighth of every token's row; xf[t] is what their sum is
+// multiplied by.  Rows with an infinity or NaN get zeros and the factor NaN.
+__device__ void split_planes(const FewArgs& a) {
     __shared__ uint32_t top[FT];  // bits of the largest magnitude: ordered as unsigned
     const int tid = threadIdx.x;
     const int d = a.d, vecs = d / RC / 8, v0 = blockIdx.y * vecs;  // 8 elements at a time
@@ -1273,24 +1308,26 @@ __device__ void rows_to_f16(const FewArgs& a) {
         uint32_t m = lane < RC ? ld_cluster_u32(map_shared_rank(smem_addr(&top[t]), lane)) : 0u;
         m = __reduce_max_sync(0xffffffffu, m);
         const bool odd = m >= 0x7F80u;
-        const int e = odd ? 0 : f16_exponent(__uint_as_float(m << 16));
+        const int e = odd ? 0 : plane_exponent(__uint_as_float(m << 16));
 #pragma unroll 2
         for (int c = lane; c < vecs; c += 32) {
             const uint4 v = x[(int64_t)t * (d / 8) + v0 + c];
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            // columns 2q, 2q + 1 of 8 (q = 0..3), the first or last 8 of 16: their place is
-            // word (8 cols & 8) / 4 + (q >> 1) of the first half or, for odd q, of the second
-            uint32_t* dst = reinterpret_cast<uint32_t*>(a.xh) +
-                            ((int64_t)t * d + ((v0 + c) >> 1) * 16) / 2 + ((v0 + c) & 1) * 2;
+            uint64_t plane[3] = {0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float lo = odd ? 0.f : scalbnf(__uint_as_float(w[q] << 16), e);
-                const float hi = odd ? 0.f : scalbnf(__uint_as_float(w[q] & 0xFFFF0000u), e);
-                const __half2 p = __floats2half2_rn(lo, hi);
-                dst[(q & 1) * 4 + (q >> 1)] = *reinterpret_cast<const uint32_t*>(&p);
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t bits = q & 1 ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16;
+                int8_t p[3];
+                digits(odd ? 0.f : scalbnf(__uint_as_float(bits), e), p);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) plane[i] |= (uint64_t)(uint8_t)p[i] << (8 * q);
             }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                *reinterpret_cast<uint64_t*>(a.xq + ((int64_t)t * 3 + i) * d + (v0 + c) * 8) = plane[i];
         }
-        if (lane == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(1.f, -e);
+        // the codes come as 16 q
+        if (lane == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(0.0625f, -e);
     }
     cluster_sync_all();  // the maxima are read before their blocks go
 }
@@ -1309,7 +1346,7 @@ __global__ void __cluster_dims__(1, RC, 1) __launch_bounds__(ROUTER_THREADS)
     pdl_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *a.status = DEV_OK;
     if ((int)blockIdx.x == (E + 7) / 8) {
-        rows_to_f16(a);
+        split_planes(a);
         return;
     }
     // two lanes share a row of W_r: four experts each
@@ -1410,6 +1447,7 @@ int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, bool pdl, cud
 template <int G>
 int launch_ffn_tokens(const FewMaps& m, const FewArgs& a, int smem_limit, bool pdl,
                       cudaStream_t st) {
+    if (G && a.T <= 2) return launch_ffn<G, G ? 2 : 8>(m, a, smem_limit, pdl, st);
     if (a.T <= 8) return launch_ffn<G, 8>(m, a, smem_limit, pdl, st);
     return launch_ffn<G, 16>(m, a, smem_limit, pdl, st);
 }

@@ -18,13 +18,12 @@ constexpr int FEW_HCAP = 512;       // hidden units a part holds in shared memor
 // ---------------------------------------------------------------- 4-bit layout
 //
 // A set is n experts (the routed ones, or the fused shared one) of hidden width
-// hid and model width d; weights are codes q in [-7, 7], sign and magnitude, and
+// hid and model width d; weights are codes q in [-7, 7] in two's complement and
 // one bf16 scale per group of G along the reduction.  Codes sit in the order in
-// which a warp's lanes take them as A fragments of f16 products (m16 x k16, lane
-// 4g + t): one 32-bit word holds a lane's eight codes of 16 columns, rows g and g +
-// 8 at columns 4t .. 4t + 3.  Fragment register i (row g + 8 (i & 1), columns 4t + 2
-// (i >> 1) and the next) is the word rotated right by 4i: bits 15 and 31 the signs,
-// 0..2 and 16..18 the magnitudes.  An f16 of those bits is q 2^-24 as it lies.
+// which a warp's lanes take them as A fragments of the 8-bit products (m16 x
+// k32, lane 4g + t): one 32-bit word holds a lane's eight codes of 16 columns, in
+// byte i the code of row g (high nibble) and of row g + 8 (low nibble) at column
+// 4t + i.  A nibble in the high half of a byte is 16 q as it lies.
 //
 // Q13: blocks [n][hid/32][d/128] of 64 rows x 128 of d: four tiles of 16 rows
 //      (tile i the gate rows of hidden units 8i..8i+7 of the 32, then their up
@@ -78,8 +77,8 @@ __host__ __device__ inline int few_parts(int W, int lightest, int heaviest, int 
 
 struct FewArgs {
     const void* x;              // [T][d] bf16
-    void* xh;                   // 4 bits: [T][d] x as f16 times a power of two, and
-    float* xf;                  // [T] what undoes that (few_router writes both)
+    int8_t* xq;                 // 4 bits: [T][3][d] planes of x, and
+    float* xf;                  // [T] what they are multiplied by (few_router writes both)
     const float* logits;        // [T][E] router logits without bias
     const float* bias;          // [E] or null
     // routed and shared weights: packed bf16, or codes (scales follow them)
@@ -105,7 +104,7 @@ struct FewArgs {
 // Upper bound on the rows of FewArgs::part for any routing of the batch.
 int64_t few_part_rows(int G, int T, int h, int E, int k, int hsum);
 // Logits z [T][E] = x Wr; clears the status word; with 4-bit weights (a.G) also
-// writes a.xh and a.xf.
+// splits x into its planes.
 int launch_few_router(const FewArgs& a, const float* Wr, float* z, bool pdl, cudaStream_t st);
 // Tensor maps of the bf16 weights (unused with 4 bits): W13 as [blocks of 128
 // rows][128][d] in boxes of 64 columns x 32 rows x 2 blocks (a granule's gate

@@ -33,70 +33,63 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
-// |w| / s rounded to nearest even, in the low 16 bits of the result: two additions, no
-// division or conversion.  |w| inv is within 2^-19 of the quotient (at most 7.03, and
-// the fast reciprocal is off by 2 ulp), and the first addition leaves it on a grid of
+// w / s rounded to nearest even, in the low bits of the result: two additions, no
+// division or conversion.  w inv is within 2^-19 of the quotient (|w / s| <= 7.03, the
+// fast reciprocal is off by 2 ulp), and the first addition leaves it on a grid of
 // 2^-11: as w and s have 8 significant bits, the quotient is n + 1/2 exactly, which it
 // stays, or at least 2^-9 away from it, on the same side after.  The second rounds to
 // integers.
-__device__ __forceinline__ uint32_t magnitude(float w, float inv) {
-    return __float_as_uint(fmaf(fabsf(w), inv, 6144.f) + (12582912.f - 6144.f));
+__device__ __forceinline__ uint32_t code_of(float w, float inv) {
+    return __float_as_uint(fmaf(w, inv, 6144.f) + (12582912.f - 6144.f));
 }
 
-constexpr uint32_t SIGNS = 0x80008000u, CODES = 0x80078007u;
+// The low bytes of four words as one.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
 
-__device__ __forceinline__ uint32_t rotl(uint32_t v, int by) { return __funnelshift_l(v, v, by); }
-__device__ __forceinline__ uint32_t rotr(uint32_t v, int by) { return __funnelshift_r(v, v, by); }
-
-// Codes of eight weights (u: their bf16, two a word, and w: in fp32) in four fragment
-// registers.
-__device__ __forceinline__ void codes_of(const uint32_t* u, const float* w, float s, uint32_t* reg) {
+// Codes of eight weights in the low nibbles of eight bytes: columns 0..3 in x.
+__device__ __forceinline__ uint2 codes_of(const float* w, float s) {
+    uint32_t q[8];
     if (s >= 1.1754944e-38f && s <= 8.5070592e37f) {  // (the fast reciprocal's range)
         const float inv = __fdividef(1.f, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reg[i] = (u[i] & SIGNS) |
-                     __byte_perm(magnitude(w[2 * i], inv), magnitude(w[2 * i + 1], inv), 0x5410);
+        for (int e = 0; e < 8; ++e) q[e] = code_of(w[e], inv);
     } else {  // no scale, or one at the end of the range
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t m[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                m[e] = s > 0.f ? (uint32_t)fminf(rintf(fabsf(w[2 * i + e]) / s), 7.f) : 0u;
-            reg[i] = (u[i] & SIGNS) | m[0] | m[1] << 16;
-        }
+        for (int e = 0; e < 8; ++e)
+            q[e] = (uint32_t)(int)(s > 0.f ? fminf(fmaxf(rintf(w[e] / s), -7.f), 7.f) : 0.f);
     }
+    return make_uint2(low_bytes(q[0], q[1], q[2], q[3]), low_bytes(q[4], q[5], q[6], q[7]));
 }
 
 // A lane's codes (row g + 8 half, columns 8c..8c + 7) to a word in fragment order:
 // lane (half, c) gets that of fragment lane 4g + 2 (c & 1) + half, 16-column step c >> 1.
-__device__ __forceinline__ uint32_t to_fragment(const uint32_t* reg, int half) {
-    const uint32_t a = rotl(reg[0] | rotl(reg[1], 8), 4 * half);  // this row's share of the
-    const uint32_t b = rotl(reg[2] | rotl(reg[3], 8), 4 * half);  // words of half 0 and 1
-    return (half ? b : a) | __shfl_xor_sync(0xffffffffu, half ? a : b, 16);
+__device__ __forceinline__ uint32_t to_fragment(uint2 codes, int half) {
+    const uint32_t mine = half ? codes.y : codes.x;
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, half ? codes.x : codes.y, 16);
+    const uint32_t hi = half ? other : mine, lo = half ? mine : other;  // rows g, g + 8
+    return (hi << 4 & 0xF0F0F0F0u) | (lo & 0x0F0F0F0Fu);
 }
 
-// The other way.
-__device__ __forceinline__ void from_fragment(uint32_t word, int half, uint32_t* reg) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, word, 16);
-    const uint32_t a = rotr(half ? other : word, 4 * half), b = rotr(half ? word : other, 4 * half);
-    reg[0] = a & CODES;
-    reg[1] = rotr(a, 8) & CODES;
-    reg[2] = b & CODES;
-    reg[3] = rotr(b, 8) & CODES;
+// The other way; the nibbles' bytes come without their sign.
+__device__ __forceinline__ uint2 from_fragment(uint32_t w, int half) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, w, 16);
+    const int shift = half ? 0 : 4;
+    const uint32_t mine = w >> shift & 0x0F0F0F0Fu, its = other >> shift & 0x0F0F0F0Fu;
+    return half ? make_uint2(its, mine) : make_uint2(mine, its);
 }
 
-// The two codes of a fragment register times s, in bf16: 128 + m as it lies, less 128, is
-// the magnitude; the product is rounded once and takes the sign.
-__device__ __forceinline__ uint32_t value_pair(uint32_t reg, __nv_bfloat162 s) {
-    const uint32_t b = (reg & 0x00070007u) | 0x43004300u;
+// Codes of two neighbouring columns (bytes 2i, 2i + 1 of n) times s, in bf16: 128 + (q +
+// 8) as it lies, less 136, is q, and the product is rounded once.
+__device__ __forceinline__ uint32_t value_pair(uint32_t n, int i, __nv_bfloat162 s) {
+    const uint32_t b = __byte_perm(n ^ 0x08080808u, 0x43434343u, i ? 0x4342 : 0x4140);
     __nv_bfloat162 v;
     memcpy(&v, &b, 4);
-    v = __hmul2(__hsub2(v, __float2bfloat162_rn(128.f)), s);
+    v = __hmul2(__hsub2(v, __float2bfloat162_rn(136.f)), s);
     uint32_t o;
     memcpy(&o, &v, 4);
-    return o ^ (reg & SIGNS);
+    return o;
 }
 
 // 16 rows x 128 columns of bf16 weights at W (ld elements a row; row i and row
@@ -124,9 +117,7 @@ __device__ __forceinline__ void block_pass(__nv_bfloat16* W, int64_t ld, int64_t
             // product by the rounded 1 / 7 rounds to the same value)
             const float s = bf16_round(group_max<G>(m) * (1.f / 7.f));
             if (c % (G / 8) == 0) *scale(c / (G / 8), g + 8 * half) = __float2bfloat16_rn(s);
-            uint32_t reg[4];
-            codes_of(u, w, s, reg);
-            *word(g) = to_fragment(reg, half);
+            *word(g) = to_fragment(codes_of(w, s), half);
         }
     } else {
         uint32_t words[8];
@@ -138,12 +129,11 @@ __device__ __forceinline__ void block_pass(__nv_bfloat16* W, int64_t ld, int64_t
         }
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-            uint32_t reg[4];
-            from_fragment(words[g], half, reg);
+            const uint2 n = from_fragment(words[g], half);
             const __nv_bfloat162 ss = __bfloat162bfloat162(s[g]);
             *reinterpret_cast<uint4*>(row + g * ld) =
-                make_uint4(value_pair(reg[0], ss), value_pair(reg[1], ss), value_pair(reg[2], ss),
-                           value_pair(reg[3], ss));
+                make_uint4(value_pair(n.x, 0, ss), value_pair(n.x, 1, ss), value_pair(n.y, 0, ss),
+                           value_pair(n.y, 1, ss));
         }
     }
 }

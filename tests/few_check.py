@@ -13,13 +13,13 @@ bound[t][c] adds up, per element:
   n_h 2^-23 sum |g H w2|             the down sum, in steps of 16 with two parts
                                      each (n_h = 2 h / 16 + parts)
 
-With 4-bit weights x and H enter as f16 times a power of two that brings the largest
-magnitude of a row (of g H: of an expert's share of a part) to [2^14, 2^15).  A bf16 is
-exact there down to f16's normal range, and below that off by at most 2^-25, 2^-39 of
-the largest; H as two parts is off by 2^-11 of 2^-11 of itself, or by that:
-      dx = 2^-39 max |x|,  da gains dx sum |w1|,  du likewise
-      dH = 2^-22 |H| + 2^-39 max |H|  in place of 2^-17 |H|
-The sums are in fp32 as before: steps of 16 within a group, then one a group.
+With 4-bit weights the products and the sums of a group are exact, and x and H are
+integers times a power of two instead: of a row of x, the largest magnitude lies
+in [2^21, 2^22) units, so that rounding moves an element by half a unit, 2^-22 of
+the largest at most; of g H the same within an expert's share of a part.  So
+      dx = 2^-22 max |x|,  da gains dx sum |w1|,  du likewise
+      dH = 2^-22 max |H|             in place of 2^-17 |H|
+(both bounds are kept, added up: the sums over groups are in fp32 as before).
 """
 
 import torch
@@ -41,12 +41,12 @@ def _ffn(x, w1, w3, w2, g, q4):
     """One expert on one token: (g * ffn(x), its bound without the gate's error)."""
     d, h = w1.shape
     a, u = x @ w1, x @ w3
-    dx = 2.0 ** -39 * x.abs().max() if q4 else 0.0
+    dx = 2.0 ** -22 * x.abs().max() if q4 else 0.0
     da = (d / 16 + 16) * 2.0 ** -23 * (x.abs() @ w1.abs()) + dx * w1.abs().sum(0)
     du = (d / 16 + 16) * 2.0 ** -23 * (x.abs() @ w3.abs()) + dx * w3.abs().sum(0)
     s = a * torch.sigmoid(a)
     H = s * u
-    stored = (2.0 ** -22 * H.abs() + 2.0 ** -39 * H.abs().max()) if q4 else 2.0 ** -17 * H.abs()
+    stored = 2.0 ** -22 * H.abs().max() if q4 else 2.0 ** -17 * H.abs()
     dH = stored + 2.0 ** -20 * H.abs() + 1.1 * u.abs() * da + s.abs() * du
     y = H @ w2
     dy = dH @ w2.abs() + (2 * h / 16 + 300) * 2.0 ** -23 * (H.abs() @ w2.abs())
