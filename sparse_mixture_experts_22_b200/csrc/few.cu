@@ -359,7 +359,9 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 // one 8-bit product, which takes the codes after two masks and a shift per 8
 // codes -- as bf16 fragments they took three shifts, four masks and four
 // subtractions, and 30 clocks per 256 weights and scheduler against 11, where HBM
-// brings 256 in 23.  Sums within a group are exact in int32; a group's scale
+// brings 256 in 23; as f16 fragments (a nibble is an f16 subnormal as it lies, one
+// column a token) they take twice the integer pipe's instructions: one token wide 63 us
+// against 54, sixteen 206 against 217.  Sums within a group are exact in int32; a group's scale
 // multiplies its sum in fp32.  A tile of 8 columns holds the planes of two
 // tokens, two tiles those of five, three those of eight.
 //
@@ -764,6 +766,14 @@ template <int TILES>
 __device__ __forceinline__ void join_planes(const float (*v)[4], float (&y)[4]) {
     const int ft = threadIdx.x & 3;
     float pair[3][4];
+    if (TILES == 1) {
+        // two tokens at most, and the first lane of a quad is the one that has them
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                pair[i][q] = i ? __shfl_sync(0xffffffffu, v[0][q], (threadIdx.x & 28) | i) : v[0][q];
+    } else
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         // pair i of lane ft is pair 3 ft + i of the group: tile (3 ft + i) / 4, lane (3 ft
@@ -1020,8 +1030,9 @@ __device__ __forceinline__ void digits(float scaled, int8_t (&p)[3]) {
     p[2] = (int8_t)((v - p[1]) >> 8);
 }
 
-// Exponent e that brings magnitudes up to m (finite) below 2^22.
-__device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? 21 - ilogbf(m) : 0; }
+// Exponent e that brings magnitudes up to m (finite) below 2^22; 2^-(e + 4) is an fp32, so
+// that the smallest rows end lower.
+__device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? min(21 - ilogbf(m), 140) : 0; }
 
 template <int G, int TT>
 __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring,
