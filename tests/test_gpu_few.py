@@ -236,6 +236,34 @@ def test_a_token_of_nan_stays_alone(group):
     assert bool((diff <= 2.0 ** -7 * clean[others].float().abs() + 1e-5).all())
 
 
+@pytest.mark.parametrize("group", [0, 32])
+def test_tokens_of_very_different_size(group):
+    """Each row is scaled by itself: neither the largest nor the smallest token moves
+    the others out of their bounds."""
+    wl = Workload("f_scale", T=4, d=256, h=128, E=2, k=2)
+    inp = I.layer_inputs(wl)
+    inp["x"] = (inp["x"].double() * torch.tensor([[2.0 ** -60], [2.0 ** -20], [2.0 ** 20],
+                                                  [2.0 ** 50]])).to(torch.bfloat16)
+    w = {n: F.quantize(inp[n].transpose(1, 2), group)[2].transpose(1, 2) if group else inp[n]
+         for n in ("w1", "w3", "w2")}
+    ref = F.layer(inp["x"], inp["Wr"], None, wl.k, w["w1"], w["w3"], w["w2"], None, None, group > 0)
+    layer, g = make_layer(wl, inp, group)
+    F.check(run(layer, g["x"]), ref)
+
+
+def test_stats_of_an_empty_batch():
+    wl, inp, _ = made("full")
+    layer, g = make_layer(wl, inp, with_stats=True)
+    run(layer, g["x"])
+    got = run(layer, g["x"][:0])
+    cfg, _, W = device_weights(wl, inp)
+    cfg = M.config_of(wl, T=0)
+    want = M.forward(cfg, g["x"][:0], g["Wr"], g["bias"], *W)
+    torch.cuda.synchronize()
+    assert torch.equal(got["stats"], want["stats"])
+    assert int(got["routed"].abs().sum()) == 0 and int(got["kept"].abs().sum()) == 0
+
+
 def test_experts_masked_by_their_bias():
     """-inf and the type's lowest value in the bias keep experts from being chosen."""
     wl, inp, _ = made("capped")
