@@ -973,30 +973,42 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
                 const int gq = (first + p) / PG - q0;
                 const int pe = min(np, (q0 + gq + 1) * PG - first);
                 const float sl = lds_bf16(sa + gq * 256), sh = lds_bf16(sa + gq * 256 + 16);
-                uint32_t f[PG][4];
+                // tiles side by side as long as their sums fit
+                constexpr int N = TILES > 3 ? 1 : TILES;
 #pragma unroll
-                for (int i = 0; i < PG; ++i) {  // (a panel past the group: zero codes)
-                    const uint2 w = p + i < pe ? cw[(p + i) * 256] : make_uint2(0, 0);
-                    codes_to_frag(w.x, w.y, f[i]);
-                }
+                for (int t0 = 0; t0 < TILES; t0 += N) {
+                    if (TILES > 3 && t0 * 8 >= 3 * s.n) break;
+                    int g[N][2][4];
 #pragma unroll
-                for (int t = 0; t < TILES; ++t) {
-                    if (TILES > 3 && t * 8 >= 3 * s.n) break;
-                    int g[2][4];
+                    for (int t = 0; t < N; ++t)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) g[0][q] = g[1][q] = 0;
+                        for (int q = 0; q < 4; ++q) g[t][0][q] = g[t][1][q] = 0;
 #pragma unroll
                     for (int i = 0; i < PG; i += 2) {  // an H fragment serves two panels
-                        uint32_t b[4];
-                        // (and its second half of the group may lie past the share)
-                        ldmatrix4(hrow[t] + (p0 + (p + i < pe ? p + i : p)) * 32, b);
-                        imma(g[0], f[i], b[0], b[1]);
-                        if (PG > 1) imma(g[1], f[(i + 1) % PG], b[2], b[3]);
+                        if (i > 0 && p + i >= pe) break;
+                        uint32_t f[2][4];
+                        const uint2 w0 = cw[(p + i) * 256];
+                        codes_to_frag(w0.x, w0.y, f[0]);
+                        if (PG > 1) {  // (a panel past the group: zero codes)
+                            const uint2 w1 = p + i + 1 < pe ? cw[(p + i + 1) * 256] : make_uint2(0, 0);
+                            codes_to_frag(w1.x, w1.y, f[1]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < N; ++t) {
+                            uint32_t b[4];
+                            ldmatrix4(hrow[t0 + t] + (p0 + p + i) * 32, b);
+                            imma(g[t][0], f[0], b[0], b[1]);
+                            if (PG > 1) imma(g[t][1], f[1], b[2], b[3]);
+                        }
                     }
-                    acc[t][0] = fmaf(small_int(g[0][0] + g[1][0]), sl, acc[t][0]);
-                    acc[t][1] = fmaf(small_int(g[0][1] + g[1][1]), sl, acc[t][1]);
-                    acc[t][2] = fmaf(small_int(g[0][2] + g[1][2]), sh, acc[t][2]);
-                    acc[t][3] = fmaf(small_int(g[0][3] + g[1][3]), sh, acc[t][3]);
+#pragma unroll
+                    for (int t = 0; t < N; ++t) {
+                        float* o = acc[t0 + t];
+                        o[0] = fmaf(small_int(g[t][0][0] + g[t][1][0]), sl, o[0]);
+                        o[1] = fmaf(small_int(g[t][0][1] + g[t][1][1]), sl, o[1]);
+                        o[2] = fmaf(small_int(g[t][0][2] + g[t][1][2]), sh, o[2]);
+                        o[3] = fmaf(small_int(g[t][0][3] + g[t][1][3]), sh, o[3]);
+                    }
                 }
                 p = pe;
             }
@@ -1031,8 +1043,12 @@ __device__ __forceinline__ void digits(float scaled, int8_t (&p)[3]) {
 }
 
 // Exponent e that brings magnitudes up to m (finite) below 2^22; 2^-(e + 4) is an fp32, so
-// that the smallest rows end lower.
+// that the smallest rows end lower.  v 2^e by two products (2^e may not be an fp32).
 __device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? min(21 - ilogbf(m), 140) : 0; }
+__device__ __forceinline__ float2 plane_factors(int e) {
+    const int some = min(e, 100);
+    return make_float2(scalbnf(1.f, some), scalbnf(1.f, e - some));
+}
 
 template <int G, int TT>
 __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* ring,
@@ -1127,12 +1143,13 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                     odd = __any_sync(0xffffffffu, odd);
                     const int e = odd ? 0 : plane_exponent(m);
+                    const float2 by = plane_factors(e);
                     int8_t* dst = reinterpret_cast<int8_t*>(Hs + warp * S::HPITCH) + lane;
 #pragma unroll
                     for (int q = 0; q < FEW_HCAP / 32; ++q)
                         if (q >= p0 && q < p1) {
                             int8_t pl[3];
-                            digits(odd ? 0.f : scalbnf(h[q], e), pl);
+                            digits(odd ? 0.f : h[q] * by.x * by.y, pl);
 #pragma unroll
                             for (int k = 0; k < 3; ++k) dst[k * S::HPLANE + q * 32] = pl[k];
                         }
@@ -1244,24 +1261,35 @@ __global__ void __launch_bounds__(CB_GROUPS * 8, 16)
     few_combine_kernel(const int4* __restrict__ table, const float* __restrict__ part,
                        __nv_bfloat16* __restrict__ out, int d, int k, int uses) {
     __shared__ float4 sums[CB_GROUPS][9];
+    __shared__ int4 use[MAX_K + 2];  // the last one ends the search for a row's use
     const int tid = threadIdx.x, col = tid & 7, grp = tid >> 3;
     const int t = blockIdx.y;
     part += blockIdx.x * CB_COLS + col * 4;
     pdl_wait();
+    if (tid <= uses)
+        use[tid] = tid < uses ? table[t * (k + 1) + tid] : make_int4(0, 0x7fffffff, 0, 0);
+    __syncthreads();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    int at = grp;  // this group's place among the rows of the use
-    for (int j = 0; j < uses; ++j) {
-        const int4 u = table[t * (k + 1) + j];
-#pragma unroll 4
-        for (; at < u.y; at += CB_GROUPS) {
-            const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)(u.x + at * u.z) * d);
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
+    // this group's rows: its place `at` among those of use j; four loads at a time
+    int at = grp, j = 0;
+    do {
+        float4 v[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b, at += CB_GROUPS) {
+            while (at >= use[j].y) at -= use[j++].y;
+            v[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < uses)
+                v[b] = *reinterpret_cast<const float4*>(part +
+                                                        (int64_t)(use[j].x + at * use[j].z) * d);
         }
-        at -= u.y;
-    }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            s.x += v[b].x;
+            s.y += v[b].y;
+            s.z += v[b].z;
+            s.w += v[b].w;
+        }
+    } while (j < uses);
     sums[grp][col] = s;
     __syncthreads();
     if (tid < CB_COLS) {
@@ -1320,6 +1348,7 @@ __device__ void split_planes(const FewArgs& a) {
         m = __reduce_max_sync(0xffffffffu, m);
         const bool odd = m >= 0x7F80u;
         const int e = odd ? 0 : plane_exponent(__uint_as_float(m << 16));
+        const float2 by = plane_factors(e);
 #pragma unroll 2
         for (int c = lane; c < vecs; c += 32) {
             const uint4 v = x[(int64_t)t * (d / 8) + v0 + c];
@@ -1329,7 +1358,7 @@ __device__ void split_planes(const FewArgs& a) {
             for (int q = 0; q < 8; ++q) {
                 const uint32_t bits = q & 1 ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16;
                 int8_t p[3];
-                digits(odd ? 0.f : scalbnf(__uint_as_float(bits), e), p);
+                digits(odd ? 0.f : __uint_as_float(bits) * by.x * by.y, p);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) plane[i] |= (uint64_t)(uint8_t)p[i] << (8 * q);
             }
