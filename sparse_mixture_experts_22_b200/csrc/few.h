@@ -55,13 +55,15 @@ int launch_q4_dequantize(const void* Q13, const void* Q2, void* W13, void* W2p, 
 // costs at one or two: where products take longer than HBM, a part holds fewer
 // granules.  With n tokens for every expert (d = 4096, h = 14336) a granule and SM takes,
 // in us, bf16 17.4 (n <= 2), 18.2 (4), 19.4 (8), 24.2 (16) and 4 bits 6.8-7.4, 9.9-11.8,
-// 15.3-18.6, 30.5-35.2; the costs are about half way between equal and these, because
-// experts with few tokens find more of HBM's rate free beside the others (16 tokens over
-// 8 experts, three draws: 242, 218, 221 us with the full ratios, 236, 203, 215 with
-// these).  At most 8 + 5/2 (n - 1), which few_part_rows counts on.
+// 15.3-18.6, 30.5-35.2; the costs lie below these ratios, because experts with few tokens
+// find more of HBM's rate free beside the others.  4 bits, mean of 16 batches in us, with
+// these, with 8 10 14 19 24, with the full ratios 8 12 18 28 36 and with equal costs: 16
+// tokens over 8 experts 200, 212, 215, 216; under a skewed router 215, 225, 242, 252; 16
+// tokens over 32 experts and shared ones 134, 133, 142, 223.  At most 8 + 5/2 (n - 1),
+// which few_part_rows counts on.
 __host__ __device__ inline int few_cost(int G, int n) {
     if (G == 0) return n <= 8 ? 8 : 10;
-    return n <= 2 ? 8 : n <= 5 ? 10 : n <= 8 ? 14 : n <= 12 ? 19 : 24;
+    return n <= 2 ? 8 : n <= 4 ? 9 : n <= 5 ? 10 : n <= 8 ? 13 : n <= 12 ? 18 : 22;
 }
 
 // Parts the experts' hidden units are cut into: W weighted granules in item order
