@@ -31,8 +31,8 @@ struct Routing {
     float g[FT * MAX_K];            // its gate
     int32_t items;                  // hit experts + the shared one
     int32_t most;                   // tokens of the one that serves most
-    int32_t W;                      // their granules, weighted
     int32_t V;                      // parts
+    int32_t q, more;                // their weighted granules over V: quotient, remainder
     int32_t expert[FEW_MAX_ITEMS];  // expert of an item, -1: shared
     int32_t n[FEW_MAX_ITEMS];       // tokens it serves
     int32_t cost[FEW_MAX_ITEMS];    // weight of a granule
@@ -43,17 +43,18 @@ struct Routing {
 };
 
 // Where part v begins, and the part that holds x, on the scale of granules weighted
-// by their items' costs: the first W % V parts are one longer than the others.
-__device__ __forceinline__ int part_start(int v, int W, int V) { return v * (W / V) + min(v, W % V); }
-__device__ __forceinline__ int part_of(int x, int W, int V) {
-    const int q = W / V, more = W % V;
-    return x < more * (q + 1) ? x / (q + 1) : more + (x - more * (q + 1)) / q;
+// by their items' costs: the first r.more parts are r.q + 1 long, the others r.q.
+__device__ __forceinline__ int part_start(const Routing& r, int v) { return v * r.q + min(v, r.more); }
+__device__ __forceinline__ int part_of(const Routing& r, int x) {
+    const int q = r.q, more = r.more, longer = more * (q + 1);
+    const bool in = x < longer;  // (one division)
+    return (in ? 0 : more) + (x - (in ? 0 : longer)) / (in ? q + 1 : q);
 }
 
 // First and last part of an item of g granules.
-__device__ __forceinline__ int first_part(const Routing& r, int i) { return part_of(r.at[i], r.W, r.V); }
+__device__ __forceinline__ int first_part(const Routing& r, int i) { return part_of(r, r.at[i]); }
 __device__ __forceinline__ int last_part(const Routing& r, int i, int g) {
-    return part_of(r.at[i] + (g - 1) * r.cost[i], r.W, r.V);
+    return part_of(r, r.at[i] + (g - 1) * r.cost[i]);
 }
 
 // Sum over this lane and the ones below.
@@ -195,8 +196,10 @@ __device__ void route_batch(const FewArgs& a, Routing& r) {
         }
         if (tid == 0) {
             r.most = most;
-            r.W = before;
-            r.V = few_parts(before, lightest, heaviest, gridDim.x);
+            const int V = few_parts(before, lightest, heaviest, gridDim.x);
+            r.V = V;
+            r.q = before / V;
+            r.more = before % V;
         }
         __syncwarp();
         before = 0;
@@ -467,7 +470,7 @@ __device__ __forceinline__ int segments(const FewArgs& a, const Routing& r, int 
     const int lane = threadIdx.x & 31;
     const int gE = a.h / FEW_GRAN, gS = a.hsum / FEW_GRAN;
     const int A = r.items - (gS > 0);
-    const int w0 = part_start(v, r.W, r.V), w1 = part_start(v + 1, r.W, r.V);
+    const int w0 = part_start(r, v), w1 = part_start(r, v + 1);
     int first = -1;  // the last item that begins at or before w0
     for (int i0 = 0; i0 < r.items; i0 += 32)
         first += __popc(__ballot_sync(0xffffffffu, i0 + lane < r.items && r.at[i0 + lane] <= w0));
