@@ -8,6 +8,7 @@ and the calls fail loudly without it.
 """
 
 import ctypes
+import functools
 import os
 from typing import Dict, List, Optional, Tuple
 
@@ -553,7 +554,7 @@ def backward(cfg: MoEConfig, grad_out, aux_coef, x, Wr, bias, W13t, W2t, W13st, 
 # ---------------------------------------------------------------- few tokens, 4-bit weights
 
 def _want(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
-    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device
+    if (t.shape != shape or t.dtype != dtype or t.device != device
             or not t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "
                          f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -567,11 +568,32 @@ def _packed_shapes(cfg: MoEConfig, shared: bool):
     return (cfg.E, 2 * cfg.h, cfg.d), (cfg.E, cfg.d, cfg.h)
 
 
+@functools.lru_cache(maxsize=256)
+def _q4_sizes(cfg: bytes, which: int, group: int) -> Tuple[int, int]:
+    return moe_q4_size(MoEConfig.from_buffer_copy(cfg), which, group)
+
+
+def _q4_convert(fn, cfg, group, shared, src, dst, stream):
+    """Calls fn (a conversion of the library) on the tensors' device; a call of a few
+    microseconds' work costs little more than the launch."""
+    dev = src[0].device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _q4_convert(fn, cfg, group, shared, src, dst, stream)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    _check(fn(ctypes.byref(cfg), 1 if shared else 0, group, src[0].data_ptr(), src[1].data_ptr(),
+              dst[0].data_ptr(), dst[1].data_ptr(), int(stream)))
+    return dst
+
+
 def quantize_weights(cfg: MoEConfig, W13, W2p, group: int = 128, shared: bool = False, out=None,
                      stream=None):
     """4-bit form (Q13, Q2) of packed bf16 weights (routed, or the fused shared
     set), into `out` if given; runs on the weights' device."""
-    sizes = moe_q4_size(cfg, 1 if shared else 0, group)
+    sizes = _q4_sizes(bytes(cfg), 1 if shared else 0, int(group))
     dev = W13.device
     if dev.type != "cuda":
         raise ValueError("expected CUDA tensors")
@@ -582,16 +604,15 @@ def quantize_weights(cfg: MoEConfig, W13, W2p, group: int = 128, shared: bool = 
         out = tuple(torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes)
     for q, name, n in zip(out, ("Q13", "Q2"), sizes):
         _want(q, name, (n,), torch.uint8, dev)
-    with torch.cuda.device(dev):
-        moe_q4_quantize(cfg, 1 if shared else 0, group, W13, W2p, *out, stream)
-    return out
+    return _q4_convert(load().moe_q4_quantize, cfg, int(group), shared, (W13, W2p), tuple(out),
+                       stream)
 
 
 def dequantize_weights(cfg: MoEConfig, Q13, Q2, group: int = 128, shared: bool = False, out=None,
                        stream=None):
     """Packed bf16 weights (W13, W2p) of a 4-bit set, into `out` if given: what
     moe_forward takes for batches longer than MOE_FEW_MAX_T."""
-    sizes = moe_q4_size(cfg, 1 if shared else 0, group)
+    sizes = _q4_sizes(bytes(cfg), 1 if shared else 0, int(group))
     dev = Q13.device
     if dev.type != "cuda":
         raise ValueError("expected CUDA tensors")
@@ -602,9 +623,8 @@ def dequantize_weights(cfg: MoEConfig, Q13, Q2, group: int = 128, shared: bool =
         out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
     for W, name, shape in zip(out, ("W13", "W2p"), shapes):
         _want(W, name, shape, torch.bfloat16, dev)
-    with torch.cuda.device(dev):
-        moe_q4_dequantize(cfg, 1 if shared else 0, group, Q13, Q2, *out, stream)
-    return out
+    return _q4_convert(load().moe_q4_dequantize, cfg, int(group), shared, (Q13, Q2), tuple(out),
+                       stream)
 
 
 class FewLayer:
