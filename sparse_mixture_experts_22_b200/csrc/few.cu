@@ -11,6 +11,8 @@
 // result does not depend on which CTA finished first.
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "few.h"
 #include "kernels.h"
@@ -1479,9 +1481,17 @@ int launch_ffn(const FewMaps& m, const FewArgs& a, int smem_limit, bool pdl, cud
     const size_t fixed = 1024 + (sizeof(Routing) + 15) / 16 * 16 + 2 * MAX_STAGES * 8 + 16;
     const int bytes = (int)((limit - fixed) / 1024 * 1024);
     auto kern = few_ffn_kernel<G, TT>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) !=
-        cudaSuccess)
-        return launch_result();
+    // once a device (the limit is the device's own)
+    static std::atomic<uint64_t> allowed{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return launch_result();
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(allowed.load(std::memory_order_acquire) & bit)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit) !=
+            cudaSuccess)
+            return launch_result();
+        allowed.fetch_or(bit, std::memory_order_release);
+    }
     launch_ex(pdl, kern, dim3(FEW_CTAS), dim3(FFN_THREADS), fixed + bytes, st, m, a, bytes);
     note_launch();
     return launch_result();
