@@ -1952,6 +1952,24 @@ static int q4_set(const moe_config* cfg, int which, int32_t group, Plan* P, int*
     return MOE_OK;
 }
 
+// The conversions read and write in any order: neither side may lie in the other.
+static int q4_apart(const Plan& P, int n, int hid, int32_t group, const void* W13, const void* W2p,
+                    const void* Q13, const void* Q2) {
+    const size_t m = (size_t)n * hid * P.d * 2;
+    const struct {
+        const void* p;
+        size_t bytes;
+    } w[2] = {{W13, 2 * m}, {W2p, m}},
+      q[2] = {{Q13, q13_bytes(n, hid, P.d, group)}, {Q2, q2_bytes(n, hid, P.d, group)}};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(w[i].p), b = reinterpret_cast<uintptr_t>(q[j].p);
+            if (a < b + q[j].bytes && b < a + w[i].bytes)
+                return fail(MOE_ERR_ARG, "the packed and the 4-bit weights overlap");
+        }
+    return MOE_OK;
+}
+
 int moe_q4_size(const moe_config* cfg, int which, int32_t group, size_t* bytes13, size_t* bytes2) {
     if (!bytes13 || !bytes2) return fail(MOE_ERR_ARG, "bytes13 or bytes2 is NULL");
     Plan P;
@@ -1971,6 +1989,7 @@ int moe_q4_quantize(const moe_config* cfg, int which, int32_t group, const void*
     MOE_TRY(need(W2p, "W2p"));
     MOE_TRY(need(Q13, "Q13"));
     MOE_TRY(need(Q2, "Q2"));
+    MOE_TRY(q4_apart(P, n, hid, group, W13, W2p, Q13, Q2));
     Device dv;
     MOE_TRY(device_facts(&dv));
     MOE_TRY(launched(launch_q4_quantize(W13, W2p, Q13, Q2, n, hid, P.d, group,
@@ -1988,6 +2007,7 @@ int moe_q4_dequantize(const moe_config* cfg, int which, int32_t group, const voi
     MOE_TRY(need(Q2, "Q2"));
     MOE_TRY(need(W13, "W13"));
     MOE_TRY(need(W2p, "W2p"));
+    MOE_TRY(q4_apart(P, n, hid, group, W13, W2p, Q13, Q2));
     Device dv;
     MOE_TRY(device_facts(&dv));
     MOE_TRY(launched(launch_q4_dequantize(Q13, Q2, W13, W2p, n, hid, P.d, group,

@@ -136,3 +136,19 @@ def test_plain_quantisation():
     assert q[0, :8].tolist() == [7, -7, 0, 2, 0, 2, 0, 6]
     z = F.quantize(torch.zeros(1, 64), 64)
     assert float(z[1]) == 0 and not z[0].any()
+
+
+@pytest.mark.parametrize("name", ["moe_q4_quantize", "moe_q4_dequantize"])
+def test_4_bit_calls_refuse_overlapping_sets(name):
+    cfg = M.make_config(4, 128, 128, 4, 2)
+    w = [1 << 30, 1 << 31]
+    sizes = [2 * 4 * 128 * 128 * 2, 4 * 128 * 128 * 2]
+    q13, q2 = M.moe_q4_size(cfg, 0, 64)
+    for i in range(2):
+        for j, q in enumerate((q13, q2)):
+            for at in (w[i], w[i] + sizes[i] - 16, w[i] - q + 16):  # each end, by 16 bytes
+                qs = [1 << 32, 1 << 33]
+                qs[j] = at
+                order = w + qs if name == "moe_q4_quantize" else qs + w
+                rc, msg = _call(name, cfg, 0, 64, *(ctypes.c_void_p(p) for p in order), None)
+                assert rc == 1 and "overlap" in msg, (i, j, rc, msg)
