@@ -332,6 +332,11 @@ __device__ __forceinline__ void codes_to_frag(uint32_t w0, uint32_t w1, uint32_t
     f[3] = (w1 << 4) & M;
 }
 
+// Orders shared memory reached by ordinary accesses and cp.async before bulk copies to it.
+__device__ __forceinline__ void fence_proxy_async() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // An integer of magnitude below 2^22 to fp32 (an addition instead of the slower
 // conversion): a group's sum is at most 128 * 112 * 128 = 1.84 million.
 __device__ __forceinline__ float small_int(int v) {
@@ -392,6 +397,8 @@ struct Shape {
     // bits then the scales of the groups they meet (one more than they fill, unless a
     // group is a panel)
     static constexpr int PANEL = Q4 ? 2048 : 8192;         // bytes of 128 rows of a panel
+    // in bf16 they end where the first half's token rows begin (4 bits: see done())
+    static_assert(Q4 || KW * KB * 128 >= 4 * PANEL, "token rows are no bulk copy's target");
     static __device__ __forceinline__ int groups(int panels) {
         return GG == 32 ? panels : panels * 32 / GG + 1;
     }
@@ -706,9 +713,17 @@ struct Consumer {
         lost = __any_sync(0xffffffffu, lost);
         return ring + (size_t)p.stage * geo.slot;
     }
+    // Gives the stage back.  FENCE: it holds token rows, and the stage's next weights may
+    // lie over them (4 bits: codes and scales of the second half reach past xoff).  The
+    // rows came by cp.async, the weights come by bulk copies, and the barriers alone do not
+    // order accesses of the two proxies.
+    template <bool FENCE>
     __device__ __forceinline__ void done() {
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[p.stage]);
+        if ((threadIdx.x & 31) == 0) {
+            if (FENCE) fence_proxy_async();
+            mbar_arrive(&empty[p.stage]);
+        }
         p.next();
     }
 };
@@ -754,7 +769,7 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
                         mma(acc[nt], f, b[nt][u / 2][2 * (u & 1)], b[nt][u / 2][2 * (u & 1) + 1]);
             }
         }
-        c.done();
+        c.done<false>();
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -873,7 +888,7 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
         } else if (left > 0) {
             block(stp, 0);
         }
-        c.done();
+        c.done<true>();
     }
 #pragma unroll
     for (int nt = 0; nt < (TILES + 2) / 3; ++nt) {
@@ -933,7 +948,7 @@ __device__ __forceinline__ void down_bf16(Consumer& c, const Seg& s, int d, bool
                 }
             }
         }
-        c.done();
+        c.done<false>();
     }
     if (mine) {
 #pragma unroll
@@ -1024,7 +1039,7 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
                 p = pe;
             }
         }
-        c.done();
+        c.done<false>();
     }
     if (!mine) return;
 #pragma unroll
