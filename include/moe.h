@@ -506,8 +506,8 @@ MOE_API int moe_q4_dequantize(const moe_config* cfg, int which, int32_t group, c
 /* moe_forward_few on 4-bit weights (Q13s / Q2s: the shared set, NULL without
  * shared experts).  The products take the values q s exactly: sums within a
  * group are exact integers, the group's scale multiplies them in fp32.  A token's
- * x enters rounded to 2^-22 of its largest magnitude, and so does H (per token,
- * expert and the units one SM holds).  A token whose x, or whose H in some expert
+ * x enters rounded to 2^-30 of its largest magnitude, and so does H (per token,
+ * expert and the units one SM holds): an x within 2^22 of the largest is exact.  A token whose x, or whose H in some expert
  * it uses, is infinite or NaN gets NaN in its row of out; the other rows do not
  * change.  MOE_ERR_ARG for another group. */
 MOE_API int moe_forward_few_q4(const moe_config* cfg, int32_t group, const void* x,

@@ -1769,7 +1769,7 @@ static int few_plan_or_fail(const moe_config* cfg, FewPlan* f) {
     const size_t T = (size_t)P.T, E = (size_t)P.E, k = (size_t)P.k;
     f->off_logits = take(T * E * 4);
     f->off_table = take(T * (k + 1) * sizeof(int4));
-    f->off_xq = take(T * 3 * (size_t)P.d);
+    f->off_xq = take(T * FEW_PLANES * (size_t)P.d);
     f->off_xf = take(T * 4);
     f->off_ppart = take(E * 4);
     f->off_hpart = take(4);

@@ -29,6 +29,7 @@ namespace moe {
 namespace {
 
 constexpr int FT = FEW_MAX_T;
+constexpr int PLANES = FEW_PLANES;
 
 // The routing of the batch, worked out by every CTA for itself (128
 // assignments at most) in shared memory.
@@ -368,18 +369,21 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 //
 // bf16 weights: m16n8k16 products with fp32 sums, H as two bf16 parts.
 //
-// 4-bit weights: the products are exact.  A row of x is an integer of 23 bits
-// times a power of two (of the row's largest magnitude: the rounding is 2^-22 of
-// that at most, what an fp32 sum of the row loses too), held as three planes of
-// signed 8-bit digits; H likewise per expert and part.  The planes are columns of
-// one 8-bit product, which takes the codes after two masks and a shift per 8
-// codes -- as bf16 fragments they took three shifts, four masks and four
-// subtractions, and 30 clocks per 256 weights and scheduler against 11, where HBM
-// brings 256 in 23; as f16 fragments (a nibble is an f16 subnormal as it lies, one
-// column a token) they take twice the integer pipe's instructions: one token wide 63 us
-// against 54, sixteen 206 against 217.  Sums within a group are exact in int32; a group's scale
-// multiplies its sum in fp32.  A tile of 8 columns holds the planes of two
-// tokens, two tiles those of five, three those of eight.
+// 4-bit weights: the products are exact.  A row of x is an integer of 31 bits
+// times a power of two (of the row's largest magnitude: the rounding is 2^-30 of
+// that at most), held as four planes of signed 8-bit digits; H likewise per expert
+// and part.  An element of x keeps its 8 bits down to 2^-22 of the largest one, and
+// one of H its 24 down to 2^-6.  (Three planes hold 23 bits: an element 10^4 times the
+// others then costs the sums of units whose codes are 0 there 10^-3 of their size, one
+// 10^5 times 10^-2, more than the bf16 store.  They take fewer tiles from five tokens
+// on, two for five and three for eight: 8 tokens over 160 experts 143 us against 153,
+// 16 tokens 206 against 230; below that the same.)  The planes are columns of one 8-bit
+// product, which takes the codes after two masks and a shift per 8 codes -- as bf16
+// fragments they took three shifts, four masks and four subtractions, and 30 clocks per
+// 256 weights and scheduler against 11, where HBM brings 256 in 23; as f16 fragments (a
+// nibble is an f16 subnormal as it lies, one column a token) they take twice the
+// integer pipe's instructions: one token wide 63 us against 54.  Sums within a group
+// are exact in int32; a group's scale multiplies its sum in fp32.
 //
 // Copied bf16 tiles are swizzled and token rows pitched by an odd multiple of 16
 // bytes, so that ldmatrix meets no bank twice; codes arrive in fragment order and
@@ -391,7 +395,7 @@ struct Shape {
     static constexpr int KW = 4;                           // warps along the columns
     static constexpr int KB = Q4 ? 128 : 64;               // least columns of a warp in a stage
     static constexpr int QB = q13_block_bytes(GG);
-    static constexpr int XROWS = Q4 ? 3 : 1;               // rows of a stage per token
+    static constexpr int XROWS = Q4 ? PLANES : 1;          // rows of a stage per token
     static constexpr int XBYTES = Q4 ? 1 : 2;              // bytes of an element
     // a stage of the second half: 2 blocks of 128 rows x panels of 32 units, with 4
     // bits then the scales of the groups they meet (one more than they fill, unless a
@@ -406,11 +410,11 @@ struct Shape {
         return 2 * panels * PANEL + (Q4 ? 2 * groups(panels) * 256 : 0);
     }
     // H: bf16 high, then low parts of the tokens' rows; 4 bits: a row first fp32, then
-    // its three planes HPLANE bytes apart (33 and 131 times 16 bytes: rows of
-    // consecutive (token, plane) meet no bank twice)
+    // its planes HPLANE bytes apart (33 and 132 times 16 bytes: the rows of two tokens'
+    // planes meet no bank twice)
     static constexpr int HPLANE = FEW_HCAP + 16;
-    static constexpr int HPITCH = Q4 ? FEW_HCAP * 4 + 48 : (FEW_HCAP + 8) * 2;
-    static_assert(!Q4 || 3 * HPLANE <= HPITCH, "the planes fit the row they replace");
+    static constexpr int HPITCH = Q4 ? PLANES * HPLANE : (FEW_HCAP + 8) * 2;
+    static_assert(!Q4 || FEW_HCAP * 4 <= HPITCH, "the planes fit the row they replace");
 };
 
 // Shared memory of one call: the ring, H and the warps' sums are sized by the most
@@ -430,10 +434,11 @@ struct Geometry {
 
 constexpr int MAX_STAGES = 12;
 
-// 4 bits: stages of two blocks of columns where three of them fit, else of one: fewer
+// 4 bits: stages of two blocks of columns where two of them fit, else of one: fewer
 // stages are fewer waits (one token, d = 4096, h = 14336, 2 of 8 experts: 54.6 us
-// against 63.8), but one of them is being read, and what the others hold has to cover
-// HBM's latency.  Eight panels always: four were slower at every size tried.
+// against 63.8).  Only where three fit: 16 tokens on that layer 243 us against 228, 8
+// over 160 experts 147.5 against 150.  Eight panels always: four were slower at every
+// size tried.
 template <typename S>
 __device__ __forceinline__ Geometry geometry(int tokens, int bytes) {
     Geometry g;
@@ -452,7 +457,7 @@ __device__ __forceinline__ Geometry geometry(int tokens, int bytes) {
         const int up = g.xoff + tokens * S::XROWS * g.xpitch;
         g.slot = (max(up, S::down(g.panels)) + 1023) / 1024 * 1024;
         g.stages = min(ring / g.slot, MAX_STAGES);
-        if (g.stages >= 3) break;
+        if (g.stages >= 2) break;
     }
     g.h = g.stages * g.slot;
     g.red = g.h + h;
@@ -782,65 +787,38 @@ __device__ __forceinline__ void up_bf16(Consumer& c, const Seg& s, int d, float*
     }
 }
 
-// Column c of the 4-bit products is token c / 3, plane c % 3: n tokens take 3 n / 8
-// tiles of 8 columns, rounded up.
-// Planes joined: v[tile][4] as the products leave them to y[4], the sums of
-// tokens 2 ft and 2 ft + 1 in the lane's two rows, as a tile of 8 tokens would
-// leave them.  A lane's tokens are columns 6 ft .. 6 ft + 5, in three lanes of a
-// quad; in each round every lane gives one pair of columns and takes one.
+// Column c of the 4-bit products is token c / 4, plane c % 4: a tile of 8 columns
+// holds two tokens.  Where its second token is past the last one, this lane's ldmatrix
+// address is to go back by so many rows: they repeat the last token's, and their
+// columns are not used.  (Up to four tiles there are as many as n needs.)
 template <int TILES>
-__device__ __forceinline__ void join_planes(const float (*v)[4], float (&y)[4]) {
-    const int ft = threadIdx.x & 3;
-    float pair[3][4];
-    if (TILES == 1) {
-        // two tokens at most, and the first lane of a quad is the one that has them
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                pair[i][q] = i ? __shfl_sync(0xffffffffu, v[0][q], (threadIdx.x & 28) | i) : v[0][q];
-    } else
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        // pair i of lane ft is pair 3 ft + i of the group: tile (3 ft + i) / 4, lane (3 ft
-        // + i) % 4; seen from the giving lane, the tile is
-        int tile = 0;
-#pragma unroll
-        for (int t = 0; t < 3; ++t)
-            if ((4 * t + ft - i + 12) % 3 == 0 && 4 * t + ft >= i && (4 * t + ft - i) / 3 < 4) tile = t;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float give = v[0][q];
-#pragma unroll
-            for (int t = 1; t < TILES; ++t) give = tile == t ? v[t][q] : give;
-            if (tile >= TILES) give = 0.f;
-            pair[i][q] = __shfl_sync(0xffffffffu, give, (threadIdx.x & 28) | ((3 * ft + i) & 3));
-        }
-    }
-#pragma unroll
-    for (int hi = 0; hi < 2; ++hi) {
-        y[2 * hi] = fmaf(pair[1][2 * hi], 65536.f, fmaf(pair[0][2 * hi + 1], 256.f, pair[0][2 * hi]));
-        y[2 * hi + 1] =
-            fmaf(pair[2][2 * hi + 1], 65536.f, fmaf(pair[2][2 * hi], 256.f, pair[1][2 * hi + 1]));
-    }
+__device__ __forceinline__ int rows_back(int t, int n) {
+    return (TILES <= 4 && t < TILES - 1) || 2 * t + 1 < n ? 0 : threadIdx.x & 4;
 }
 
-// The same for 4 bits; TILES: tiles of 8 columns, up to three all computed, so that
+// The planes of a tile joined, the highest with weight 1.  A lane holds two planes of
+// token ft / 2 (ft = lane & 3; low ones where ft is even) in rows lane / 4 and lane / 4
+// + 8; it gets the sum of row lane / 4 + 8 (ft & 1).
+__device__ __forceinline__ float join_planes(const float (&v)[4]) {
+    constexpr float D = 1.f / 256.f;
+    const bool high = threadIdx.x & 1;
+    const float up = fmaf(v[0], D, v[1]), down = fmaf(v[2], D, v[3]);
+    const float other = __shfl_xor_sync(0xffffffffu, high ? up : down, 1);
+    return high ? fmaf(other, D * D, down) : fmaf(up, D * D, other);
+}
+
+// The same for 4 bits; TILES: tiles of 8 columns, up to four all computed, so that
 // their products overlap.
 template <int G, int TT, int TILES>
 __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* red) {
     using S = Shape<G, TT>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kw = warp & 3, gw = warp >> 2;
-    const int lm = lane & 7, lq = lane >> 3;
-    uint32_t xrow[TILES];
+    const uint32_t xrow = c.geo.xoff + (lane & 7) * c.geo.xpitch + kw * c.geo.blocks * 128 + (lane >> 3) * 16;
     float acc[TILES][4];
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-        const int row = min(t * 8 + lm, 3 * s.n - 1);
-        xrow[t] = c.geo.xoff + row * c.geo.xpitch + kw * c.geo.blocks * 128 + lq * 16;
+    for (int t = 0; t < TILES; ++t)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
-    }
     auto block = [&](const uint8_t* stp, int kb) {
         const int blk = kw * c.geo.blocks + kb;
         const uint4* cw = reinterpret_cast<const uint4*>(stp + blk * S::QB + gw * 1024);
@@ -862,10 +840,11 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
         }
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            if (TILES > 3 && t * 8 >= 3 * s.n) break;
+            if (TILES > 4 && 2 * t >= s.n) break;
+            const uint32_t at = st + xrow + (t * 8 - rows_back<TILES>(t, s.n)) * c.geo.xpitch + kb * 128;
             uint32_t b[2][4];
-            ldmatrix4(st + xrow[t] + kb * 128, b[0]);
-            ldmatrix4(st + xrow[t] + kb * 128 + 64, b[1]);
+            ldmatrix4(at, b[0]);
+            ldmatrix4(at + 64, b[1]);
 #pragma unroll
             for (int q = 0; q < 128 / S::GG; ++q) {
                 int g[4] = {0, 0, 0, 0};
@@ -890,15 +869,12 @@ __device__ __forceinline__ void up_q4(Consumer& c, const Seg& s, int d, float* r
         }
         c.done<true>();
     }
+    // (20 floats a token)
+    red += ((lane & 3) >> 1) * 20 + (lane & 1) * 8 + (lane >> 2);
 #pragma unroll
-    for (int nt = 0; nt < (TILES + 2) / 3; ++nt) {
-        float y[4];
-        join_planes<(TILES < 3 ? TILES : 3)>(acc + 3 * nt, y);
-        float* q = red + nt * 160 + 2 * (lane & 3) * 20 + (lane >> 2);
-        q[0] = y[0];
-        q[20] = y[1];
-        q[8] = y[2];
-        q[28] = y[3];
+    for (int t = 0; t < TILES; ++t) {
+        if (TILES > 4 && 2 * t >= s.n) break;
+        red[t * 40] = join_planes(acc[t]);
     }
 }
 
@@ -974,16 +950,12 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
     using S = Shape<G, TT>;
     constexpr int PG = S::GG / 32;  // panels of a group
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rb = warp >> 3, tile = warp & 7;
-    const int lm = lane & 7, lq = lane >> 3, ft = lane & 3;
-    uint32_t hrow[TILES];
+    const uint32_t hrow = hs + (lane & 7) * S::HPLANE + s.hb + (lane >> 3) * 16;
     float acc[TILES][4];
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-        const int row = min(t * 8 + lm, 3 * s.n - 1);
-        hrow[t] = hs + row / 3 * S::HPITCH + row % 3 * S::HPLANE + s.hb + lq * 16;
+    for (int t = 0; t < TILES; ++t)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
-    }
     const int step = s.step(c.geo.panels);
     for (int p0 = 0; p0 < s.len / 32; p0 += step) {
         const int np = min(step, s.len / 32 - p0);
@@ -1000,10 +972,10 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
                 const int pe = min(np, (q0 + gq + 1) * PG - first);
                 const float sl = lds_bf16(sa + gq * 256), sh = lds_bf16(sa + gq * 256 + 16);
                 // tiles side by side as long as their sums fit
-                constexpr int N = TILES > 3 ? 1 : TILES;
+                constexpr int N = TILES == 4 ? 2 : TILES > 4 ? 1 : TILES;
 #pragma unroll
                 for (int t0 = 0; t0 < TILES; t0 += N) {
-                    if (TILES > 3 && t0 * 8 >= 3 * s.n) break;
+                    if (TILES > 4 && 2 * t0 >= s.n) break;
                     int g[N][2][4];
 #pragma unroll
                     for (int t = 0; t < N; ++t)
@@ -1022,7 +994,8 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
 #pragma unroll
                         for (int t = 0; t < N; ++t) {
                             uint32_t b[4];
-                            ldmatrix4(hrow[t0 + t] + (p0 + p + i) * 32, b);
+                            const int row = (t0 + t) * 8 - rows_back<TILES>(t0 + t, s.n);
+                            ldmatrix4(hrow + row * S::HPLANE + (p0 + p + i) * 32, b);
                             imma(g[t][0], f[0], b[0], b[1]);
                             if (PG > 1) imma(g[t][1], f[1], b[2], b[3]);
                         }
@@ -1043,34 +1016,31 @@ __device__ __forceinline__ void down_q4(Consumer& c, const Seg& s, int d, bool m
     }
     if (!mine) return;
 #pragma unroll
-    for (int nt = 0; nt < (TILES + 2) / 3; ++nt) {
-        float y[4];
-        join_planes<(TILES < 3 ? TILES : 3)>(acc + 3 * nt, y);
-        const int n = nt * 8 + 2 * ft;
-        float* q = out + (int64_t)n * d;
-        if (n < s.n) {
-            q[0] = y[0] * hf[n];
-            q[8] = y[2] * hf[n];
-        }
-        if (n + 1 < s.n) {
-            q[d] = y[1] * hf[n + 1];
-            q[d + 8] = y[3] * hf[n + 1];
-        }
+    for (int t = 0; t < TILES; ++t) {
+        if (TILES > 4 && 2 * t >= s.n) break;
+        const float y = join_planes(acc[t]);
+        const int n = 2 * t + ((lane & 3) >> 1);
+        if (n < s.n) out[(int64_t)n * d + (lane & 1) * 8] = y * hf[n];
     }
 }
 
-// v 2^e as three signed digits of 8 bits, low first (|v 2^e| < 2^22).
-__device__ __forceinline__ void digits(float scaled, int8_t (&p)[3]) {
+// A value below 2^30 as signed digits of 8 bits, low first.
+__device__ __forceinline__ void digits(float scaled, int8_t (&p)[PLANES]) {
     int v = __float2int_rn(scaled);
-    p[0] = (int8_t)v;
-    v = (v - p[0]) >> 8;
-    p[1] = (int8_t)v;
-    p[2] = (int8_t)((v - p[1]) >> 8);
+#pragma unroll
+    for (int i = 0; i < PLANES; ++i) {
+        p[i] = (int8_t)v;
+        v = (v - p[i]) >> 8;
+    }
 }
 
-// Exponent e that brings magnitudes up to m (finite) below 2^22; 2^-(e + 4) is an fp32, so
-// that the smallest rows end lower.  v 2^e by two products (2^e may not be an fp32).
-__device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? min(21 - ilogbf(m), 140) : 0; }
+// Exponent e that brings magnitudes up to m (finite) to [2^29, 2^30); the smallest end
+// lower, where every fp32 is a whole number already.  v 2^e by two products (2^e may not
+// be an fp32).
+__device__ __forceinline__ int plane_exponent(float m) { return m > 0.f ? min(29 - ilogbf(m), 160) : 0; }
+// What the joined planes' products are multiplied by: the codes come as 16 q, and the
+// highest plane counts 2^24.
+__device__ __forceinline__ float plane_unit(int e) { return scalbnf(1.f, 20 - e); }
 __device__ __forceinline__ float2 plane_factors(int e) {
     const int some = min(e, 100);
     return make_float2(scalbnf(1.f, some), scalbnf(1.f, e - some));
@@ -1115,12 +1085,14 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                     up_bf16<TT>(c, s, d, mine);
                 else if (TT <= 2 || s.n <= 2)
                     up_q4<G, TT, 1>(c, s, d, mine);
-                else if (s.n <= 5)
+                else if (s.n <= 4)
                     up_q4<G, TT, TT <= 2 ? 1 : 2>(c, s, d, mine);
-                else if (TT <= 8 || s.n <= 8)
+                else if (s.n <= 6)
                     up_q4<G, TT, TT <= 2 ? 1 : 3>(c, s, d, mine);
+                else if (TT <= 8 || s.n <= 8)
+                    up_q4<G, TT, TT <= 2 ? 1 : 4>(c, s, d, mine);
                 else
-                    up_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 3 : 6>(c, s, d, mine);
+                    up_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 4 : 8>(c, s, d, mine);
                 named_sync(2 + gw, 128);
                 if (n < s.n) {
                     float ga = 0.f, up = 0.f;
@@ -1174,12 +1146,12 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
 #pragma unroll
                     for (int q = 0; q < FEW_HCAP / 32; ++q)
                         if (q >= p0 && q < p1) {
-                            int8_t pl[3];
+                            int8_t pl[PLANES];
                             digits(odd ? 0.f : h[q] * by.x * by.y, pl);
 #pragma unroll
-                            for (int k = 0; k < 3; ++k) dst[k * S::HPLANE + q * 32] = pl[k];
+                            for (int k = 0; k < PLANES; ++k) dst[k * S::HPLANE + q * 32] = pl[k];
                         }
-                    if (lane == 0) hf[i][warp] = odd ? NAN : scalbnf(0.0625f, -e);
+                    if (lane == 0) hf[i][warp] = odd ? NAN : plane_unit(e);
                 }
             }
             named_sync(1, CONSUMERS);
@@ -1196,12 +1168,14 @@ __device__ void consume(const FewArgs& a, const Routing& r, Seg* segs, uint8_t* 
                     down_bf16<TT>(c, s, d, mine, hs, out);
                 else if (TT <= 2 || s.n <= 2)
                     down_q4<G, TT, 1>(c, s, d, mine, hs, hf[i], out);
-                else if (s.n <= 5)
+                else if (s.n <= 4)
                     down_q4<G, TT, TT <= 2 ? 1 : 2>(c, s, d, mine, hs, hf[i], out);
-                else if (TT <= 8 || s.n <= 8)
+                else if (s.n <= 6)
                     down_q4<G, TT, TT <= 2 ? 1 : 3>(c, s, d, mine, hs, hf[i], out);
+                else if (TT <= 8 || s.n <= 8)
+                    down_q4<G, TT, TT <= 2 ? 1 : 4>(c, s, d, mine, hs, hf[i], out);
                 else
-                    down_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 3 : 6>(c, s, d, mine, hs, hf[i], out);
+                    down_q4<G, TT, TT <= 2 ? 1 : TT <= 8 ? 4 : 8>(c, s, d, mine, hs, hf[i], out);
             }
         }
     }
@@ -1379,21 +1353,20 @@ __device__ void split_planes(const FewArgs& a) {
         for (int c = lane; c < vecs; c += 32) {
             const uint4 v = x[(int64_t)t * (d / 8) + v0 + c];
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint64_t plane[3] = {0, 0, 0};
+            uint64_t plane[PLANES] = {};
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const uint32_t bits = q & 1 ? w[q / 2] & 0xFFFF0000u : w[q / 2] << 16;
-                int8_t p[3];
+                int8_t p[PLANES];
                 digits(odd ? 0.f : __uint_as_float(bits) * by.x * by.y, p);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) plane[i] |= (uint64_t)(uint8_t)p[i] << (8 * q);
+                for (int i = 0; i < PLANES; ++i) plane[i] |= (uint64_t)(uint8_t)p[i] << (8 * q);
             }
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                *reinterpret_cast<uint64_t*>(a.xq + ((int64_t)t * 3 + i) * d + (v0 + c) * 8) = plane[i];
+            for (int i = 0; i < PLANES; ++i)
+                *reinterpret_cast<uint64_t*>(a.xq + ((int64_t)t * PLANES + i) * d + (v0 + c) * 8) = plane[i];
         }
-        // the codes come as 16 q
-        if (lane == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : scalbnf(0.0625f, -e);
+        if (lane == 0 && blockIdx.y == 0) a.xf[t] = odd ? NAN : plane_unit(e);
     }
     cluster_sync_all();  // the maxima are read before their blocks go
 }

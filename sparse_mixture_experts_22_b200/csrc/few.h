@@ -14,6 +14,7 @@ constexpr int FEW_CTAS = 148;       // CTAs of the expert kernel (one per SM)
 constexpr int FEW_MAX_ITEMS = FEW_MAX_T * 8 + 1;  // experts one batch can hit, and the shared one
 constexpr int FEW_GRAN = 32;        // hidden units per granule, the unit the CTAs share work in
 constexpr int FEW_HCAP = 512;       // hidden units a part holds in shared memory at most
+constexpr int FEW_PLANES = 4;       // 8-bit digits of an element of x or H beside 4-bit weights
 
 // ---------------------------------------------------------------- 4-bit layout
 //
@@ -54,16 +55,16 @@ int launch_q4_dequantize(const void* Q13, const void* Q2, void* W13, void* W2p, 
 // What a granule costs an SM when its expert serves n tokens, in eighths of what it
 // costs at one or two: where products take longer than HBM, a part holds fewer
 // granules.  With n tokens for every expert (d = 4096, h = 14336) a granule and SM takes,
-// in us, bf16 17.4 (n <= 2), 18.2 (4), 19.4 (8), 24.2 (16) and 4 bits 6.8-7.4, 9.9-11.8,
-// 15.3-18.6, 30.5-35.2; the costs lie below these ratios, because experts with few tokens
-// find more of HBM's rate free beside the others.  4 bits, mean of 16 batches in us, with
-// these, with 8 10 14 19 24, with the full ratios 8 12 18 28 36 and with equal costs: 16
-// tokens over 8 experts 200, 212, 215, 216; under a skewed router 215, 225, 242, 252; 16
-// tokens over 32 experts and shared ones 134, 133, 142, 223.  At most 8 + 5/2 (n - 1),
-// which few_part_rows counts on.
+// in us, bf16 16.7-17.0 (n <= 2), 17.1-18.0 (4), 18.6-18.9 (8), 23.1 (16) and 4 bits
+// 5.9-6.9, 7.3-9.7, 13.9-19.1, 35.6-39.5; the costs lie below these ratios, because
+// experts with few tokens find more of HBM's rate free beside the others.  4 bits, mean
+// of 16 batches in us, with these, with 8 9 12 14 19 24 and with 8 10 13 18 23 28: 8
+// tokens over 160 experts and shared ones 147, 160, 151; 16 tokens over 8 experts 243,
+// 242, 243; under a skewed router 255, 247, 262; 16 tokens over 32 experts and shared
+// ones 153, 155, 156.  At most 8 + 5/2 (n - 1), which few_part_rows counts on.
 __host__ __device__ inline int few_cost(int G, int n) {
     if (G == 0) return n <= 8 ? 8 : 10;
-    return n <= 2 ? 8 : n <= 4 ? 9 : n <= 5 ? 10 : n <= 8 ? 13 : n <= 12 ? 18 : 22;
+    return n <= 2 ? 8 : n <= 4 ? 10 : n <= 6 ? 13 : n <= 8 ? 15 : n <= 12 ? 21 : 26;
 }
 
 // Parts the experts' hidden units are cut into: W weighted granules in item order
@@ -79,7 +80,7 @@ __host__ __device__ inline int few_parts(int W, int lightest, int heaviest, int 
 
 struct FewArgs {
     const void* x;              // [T][d] bf16
-    int8_t* xq;                 // 4 bits: [T][3][d] planes of x, and
+    int8_t* xq;                 // 4 bits: [T][FEW_PLANES][d] planes of x, and
     float* xf;                  // [T] what they are multiplied by (few_router writes both)
     const float* logits;        // [T][E] router logits without bias
     const float* bias;          // [E] or null
