@@ -159,6 +159,15 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _stream_on(stream, device) -> torch.cuda.Stream:
+    """The torch stream that a stream argument names: a torch stream or an address."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if int(stream) == 0:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
 # ---------------------------------------------------------------- config
 
 OVERFLOW = {"drop": 0, "reroute": 1}
@@ -573,26 +582,34 @@ def _q4_sizes(cfg: bytes, which: int, group: int) -> Tuple[int, int]:
     return moe_q4_size(MoEConfig.from_buffer_copy(cfg), which, group)
 
 
-def _q4_convert(fn, cfg, group, shared, src, dst, stream):
+def _q4_convert(fn, cfg, group, shared, src, dst, fresh, stream):
     """Calls fn (a conversion of the library) on the tensors' device; a call of a few
-    microseconds' work costs little more than the launch."""
+    microseconds' work costs little more than the launch.  dst was allocated on the current
+    stream if fresh: another stream waits for what that one still does with the memory,
+    and the memory of a call on a given stream is not handed out again before it ends."""
     dev = src[0].device
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            return _q4_convert(fn, cfg, group, shared, src, dst, stream)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
+            return _q4_convert(fn, cfg, group, shared, src, dst, fresh, stream)
+    current = torch.cuda.current_stream(dev)
+    on = current if stream is None else _stream_on(stream, dev)
+    if fresh and on != current:
+        on.wait_stream(current)
     _check(fn(ctypes.byref(cfg), 1 if shared else 0, group, src[0].data_ptr(), src[1].data_ptr(),
-              dst[0].data_ptr(), dst[1].data_ptr(), int(stream)))
+              dst[0].data_ptr(), dst[1].data_ptr(), on.cuda_stream))
+    if stream is not None:
+        for t in (*src, *dst):
+            t.record_stream(on)
     return dst
 
 
 def quantize_weights(cfg: MoEConfig, W13, W2p, group: int = 128, shared: bool = False, out=None,
                      stream=None):
     """4-bit form (Q13, Q2) of packed bf16 weights (routed, or the fused shared
-    set), into `out` if given; runs on the weights' device."""
+    set), into `out` if given; runs on the weights' device, on its current stream
+    unless one is given.  A given stream is ordered after the current one if the
+    result is allocated here; otherwise, and where the result is read, the order is
+    the caller's."""
     sizes = _q4_sizes(bytes(cfg), 1 if shared else 0, int(group))
     dev = W13.device
     if dev.type != "cuda":
@@ -600,18 +617,20 @@ def quantize_weights(cfg: MoEConfig, W13, W2p, group: int = 128, shared: bool = 
     for W, name, shape in zip((W13, W2p), ("W13", "W2p"), _packed_shapes(cfg, shared)):
         # the shared set may come with a leading 1, as one expert of the routed layout
         _want(W.squeeze(0) if shared and W.dim() == 3 else W, name, shape, torch.bfloat16, dev)
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = tuple(torch.empty(n, dtype=torch.uint8, device=dev) for n in sizes)
     for q, name, n in zip(out, ("Q13", "Q2"), sizes):
         _want(q, name, (n,), torch.uint8, dev)
     return _q4_convert(load().moe_q4_quantize, cfg, int(group), shared, (W13, W2p), tuple(out),
-                       stream)
+                       fresh, stream)
 
 
 def dequantize_weights(cfg: MoEConfig, Q13, Q2, group: int = 128, shared: bool = False, out=None,
                        stream=None):
     """Packed bf16 weights (W13, W2p) of a 4-bit set, into `out` if given: what
-    moe_forward takes for batches longer than MOE_FEW_MAX_T."""
+    moe_forward takes for batches longer than MOE_FEW_MAX_T.  Device and streams as in
+    quantize_weights."""
     sizes = _q4_sizes(bytes(cfg), 1 if shared else 0, int(group))
     dev = Q13.device
     if dev.type != "cuda":
@@ -619,12 +638,13 @@ def dequantize_weights(cfg: MoEConfig, Q13, Q2, group: int = 128, shared: bool =
     for q, name, n in zip((Q13, Q2), ("Q13", "Q2"), sizes):
         _want(q, name, (n,), torch.uint8, dev)
     shapes = _packed_shapes(cfg, shared)
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = tuple(torch.empty(s, dtype=torch.bfloat16, device=dev) for s in shapes)
     for W, name, shape in zip(out, ("W13", "W2p"), shapes):
         _want(W, name, shape, torch.bfloat16, dev)
     return _q4_convert(load().moe_q4_dequantize, cfg, int(group), shared, (Q13, Q2), tuple(out),
-                       stream)
+                       fresh, stream)
 
 
 class FewLayer:
@@ -637,7 +657,10 @@ class FewLayer:
     stats), overwritten by the next call.  The capacity of a call counts its t
     tokens.  A call runs on the weights' device and, unless a stream is given,
     on that device's current stream; the layer's buffers are shared by its
-    calls, so calls on several streams must be ordered by the caller."""
+    calls, so calls on several streams must be ordered by the caller, as must the
+    inputs.  Memory is not handed out again under a call: the constructor waits for
+    the work that its stream still has for the memory of its buffers, and those, the
+    weights and an x passed with a stream are kept until the calls' streams are done."""
 
     def __init__(self, cfg: MoEConfig, Wr, bias, W13, W2p, W13s=None, W2s=None,
                  group: Optional[int] = None, with_stats: bool = False):
@@ -661,7 +684,7 @@ class FewLayer:
         _want(Wr, "Wr", (cfg.d, cfg.E), torch.float32, dev)
         if cfg.has_bias:
             _want(bias, "bias", (cfg.E,), torch.float32, dev)
-        self._held = (Wr, bias, *weights)
+        self._held = (Wr, bias if cfg.has_bias else None, *weights)
         T, E, k, d = cfg.T, cfg.E, cfg.k, cfg.d
         self.bufs = {
             "out": torch.empty((T, d), dtype=torch.bfloat16, device=dev),
@@ -676,6 +699,10 @@ class FewLayer:
         need = max(moe_few_workspace_size(self._config(t)) for t in range(T + 1))
         self.ws = torch.empty(need, dtype=torch.uint8, device=dev)
         self._calls: Dict[int, tuple] = {}
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+        self._streams: Dict[int, torch.cuda.Stream] = {}  # those that the memory is kept for
 
     def _config(self, t: int) -> MoEConfig:
         c = MoEConfig.from_buffer_copy(self.cfg)
@@ -711,11 +738,16 @@ class FewLayer:
         return self._run(fn, head, tail, views, x, stream)
 
     def _run(self, fn, head, tail, views, x, stream):
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device).cuda_stream
-        elif isinstance(stream, torch.cuda.Stream):
-            stream = stream.cuda_stream
-        rc = fn(*head, x.data_ptr(), *tail, stream)
+        on = torch.cuda.current_stream(self.device) if stream is None else stream
+        handle = on.cuda_stream if isinstance(on, torch.cuda.Stream) else int(on)
+        if handle not in self._streams:
+            on = self._streams[handle] = _stream_on(on, self.device)
+            for t in (*self._held, *self.bufs.values(), self.ws):
+                if t is not None:
+                    t.record_stream(on)
+        rc = fn(*head, x.data_ptr(), *tail, handle)
         if rc:
             _check(rc)
+        if stream is not None:
+            x.record_stream(self._streams[handle])
         return views
