@@ -668,6 +668,7 @@ class FewLayer:
         if dev.type != "cuda":
             raise ValueError("expected CUDA tensors")
         self._lib = load()
+        cfg = MoEConfig.from_buffer_copy(cfg)  # the caller's may change
         self.cfg, self.group, self.device = cfg, group, dev
         moe_few_workspace_size(cfg)  # refuses what the layer does not take
         weights = [W13, W2p] + ([W13s, W2s] if cfg.n_shared else [])
