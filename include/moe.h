@@ -492,10 +492,11 @@ MOE_API int moe_forward_few(const moe_config* cfg, const void* x, const float* W
  * moe_q4_quantize makes one set from packed bf16 weights: which = 0 the routed
  * experts (W13 [E][2h][d], W2p [E][d][h]), which = 1 the fused shared expert,
  * both as moe_pack_weights leaves them; weights must be finite.  Q13 and Q2 take
- * the bytes moe_q4_size gives; their layout is the library's own.  Neither may
- * overlap the packed weights (MOE_ERR_ARG).
+ * the bytes moe_q4_size gives; their layout is the library's own.  They may
+ * overlap neither the packed weights nor each other (MOE_ERR_ARG).
  * moe_q4_dequantize writes the values, rounded once to bf16, in the packed
- * layout: moe_forward on them is the layer for batches of any length.  */
+ * layout: moe_forward on them is the layer for batches of any length.  W13 and W2p
+ * may overlap neither the 4-bit weights nor each other (MOE_ERR_ARG). */
 MOE_API int moe_q4_size(const moe_config* cfg, int which, int32_t group, size_t* bytes13,
                         size_t* bytes2);
 MOE_API int moe_q4_quantize(const moe_config* cfg, int which, int32_t group, const void* W13,

@@ -1952,20 +1952,26 @@ static int q4_set(const moe_config* cfg, int which, int32_t group, Plan* P, int*
     return MOE_OK;
 }
 
-// The conversions read and write in any order: neither side may lie in the other.
+// A conversion reads and writes in any order: none of what it writes may lie in what it
+// reads or in the other thing it writes.
 static int q4_apart(const Plan& P, int n, int hid, int32_t group, const void* W13, const void* W2p,
-                    const void* Q13, const void* Q2) {
+                    const void* Q13, const void* Q2, bool quantize) {
     const size_t m = (size_t)n * hid * P.d * 2;
     const struct {
         const void* p;
         size_t bytes;
-    } w[2] = {{W13, 2 * m}, {W2p, m}},
-      q[2] = {{Q13, q13_bytes(n, hid, P.d, group)}, {Q2, q2_bytes(n, hid, P.d, group)}};
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j) {
-            const uintptr_t a = reinterpret_cast<uintptr_t>(w[i].p), b = reinterpret_cast<uintptr_t>(q[j].p);
-            if (a < b + q[j].bytes && b < a + w[i].bytes)
-                return fail(MOE_ERR_ARG, "the packed and the 4-bit weights overlap");
+        bool written;
+        const char* name;
+    } set[4] = {{W13, 2 * m, !quantize, "W13"},
+                {W2p, m, !quantize, "W2p"},
+                {Q13, q13_bytes(n, hid, P.d, group), quantize, "Q13"},
+                {Q2, q2_bytes(n, hid, P.d, group), quantize, "Q2"}};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(set[i].p),
+                            b = reinterpret_cast<uintptr_t>(set[j].p);
+            if ((set[i].written || set[j].written) && a < b + set[j].bytes && b < a + set[i].bytes)
+                return fail(MOE_ERR_ARG, "%s and %s overlap", set[i].name, set[j].name);
         }
     return MOE_OK;
 }
@@ -1989,7 +1995,7 @@ int moe_q4_quantize(const moe_config* cfg, int which, int32_t group, const void*
     MOE_TRY(need(W2p, "W2p"));
     MOE_TRY(need(Q13, "Q13"));
     MOE_TRY(need(Q2, "Q2"));
-    MOE_TRY(q4_apart(P, n, hid, group, W13, W2p, Q13, Q2));
+    MOE_TRY(q4_apart(P, n, hid, group, W13, W2p, Q13, Q2, true));
     Device dv;
     MOE_TRY(device_facts(&dv));
     MOE_TRY(launched(launch_q4_quantize(W13, W2p, Q13, Q2, n, hid, P.d, group,
@@ -2007,7 +2013,7 @@ int moe_q4_dequantize(const moe_config* cfg, int which, int32_t group, const voi
     MOE_TRY(need(Q2, "Q2"));
     MOE_TRY(need(W13, "W13"));
     MOE_TRY(need(W2p, "W2p"));
-    MOE_TRY(q4_apart(P, n, hid, group, W13, W2p, Q13, Q2));
+    MOE_TRY(q4_apart(P, n, hid, group, W13, W2p, Q13, Q2, false));
     Device dv;
     MOE_TRY(device_facts(&dv));
     MOE_TRY(launched(launch_q4_dequantize(Q13, Q2, W13, W2p, n, hid, P.d, group,
