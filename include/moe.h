@@ -470,8 +470,11 @@ MOE_API int moe_route_static(const moe_config* cfg, const void* x, const float* 
  * Mixtral 8x7B and MoE explained, "Easy explanation" ¶4].  Arguments as in
  * moe_forward, without slot_of; three launches, and two more with stats (which
  * may be NULL).  H stays on the chip and reaches the down projection as two bf16
- * parts whatever cfg->hidden_mode says.  Routing outputs equal moe_forward's
- * (gates to fp32 rounding); repeated calls give identical bits.
+ * parts whatever cfg->hidden_mode says.  Logits are fp32 sums in another order
+ * than moe_forward's: the choice of experts is the same except where logits lie
+ * within the rounding of such a sum of one another, and with it routed, kept and
+ * the assignments that a capacity drops; gates agree to that rounding.  Repeated
+ * calls give identical bits.
  * Errors besides those of every call, before any launch: MOE_ERR_SHAPE for
  * T > MOE_FEW_MAX_T, MOE_ERR_DTYPE for an fp32 config, MOE_ERR_UNSUPPORTED for
  * the reroute policy or train = 1.  ws: moe_few_workspace_size(cfg) bytes,
@@ -508,9 +511,12 @@ MOE_API int moe_q4_dequantize(const moe_config* cfg, int which, int32_t group, c
  * shared experts).  The products take the values q s exactly: sums within a
  * group are exact integers, the group's scale multiplies them in fp32.  A token's
  * x enters rounded to 2^-30 of its largest magnitude, and so does H (per token,
- * expert and the units one SM holds): an x within 2^22 of the largest is exact.  A token whose x, or whose H in some expert
- * it uses, is infinite or NaN gets NaN in its row of out; the other rows do not
- * change.  MOE_ERR_ARG for another group. */
+ * expert and the units one SM holds): an x within 2^22 of the largest is exact.
+ * A token whose x, or whose H in some expert it uses, is infinite or NaN gets NaN
+ * in its row of out.  It still chooses experts (NaN logits count as -inf) and takes
+ * its places under a capacity; the other rows are those of any batch with these
+ * choices, cut into parts, and so summed, in another order.  MOE_ERR_ARG for
+ * another group. */
 MOE_API int moe_forward_few_q4(const moe_config* cfg, int32_t group, const void* x,
                                const float* Wr, const float* bias, const void* Q13,
                                const void* Q2, const void* Q13s, const void* Q2s, void* out,
