@@ -562,7 +562,9 @@ def backward(cfg: MoEConfig, grad_out, aux_coef, x, Wr, bias, W13t, W2t, W13st, 
 
 # ---------------------------------------------------------------- few tokens, 4-bit weights
 
-def _want(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
+def _want(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        raise ValueError(f"{name} is missing")
     if (t.shape != shape or t.dtype != dtype or t.device != device
             or not t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} "

@@ -1,4 +1,4 @@
-"""A FewLayer keeps to the config it was made with."""
+"""A FewLayer keeps to the config it was made with, and refuses what it lacks."""
 
 import pytest
 import torch
@@ -29,3 +29,15 @@ def test_a_config_changed_later(group):
     with pytest.raises(ValueError):
         seen(torch.zeros((wl.T + 1, wl.d), dtype=torch.bfloat16, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("missing", ["bias", "W13", "W2p", "W13s", "W2s"])
+def test_missing_inputs(missing):
+    wl, inp, _ = made("shared")
+    cfg, g, W = device_weights(wl, inp)
+    cfg.has_bias = 1
+    args = dict(zip(("bias", "W13", "W2p", "W13s", "W2s"), (torch.zeros(wl.E, device="cuda"), *W)))
+    M.FewLayer(cfg, g["Wr"], **args)
+    args[missing] = None
+    with pytest.raises(ValueError):
+        M.FewLayer(cfg, g["Wr"], **args)
