@@ -168,6 +168,23 @@ def _stream_on(stream, device) -> torch.cuda.Stream:
     return torch.cuda.ExternalStream(int(stream), device=device)
 
 
+def _after_current(stream, device):
+    """Orders a given stream after the current one, whose memory has just been allocated."""
+    if stream is not None:
+        on, current = _stream_on(stream, device), torch.cuda.current_stream(device)
+        if on != current:
+            on.wait_stream(current)
+
+
+def _keep(stream, device, tensors):
+    """Keeps the tensors' memory until a given stream is done with what it has now."""
+    if stream is not None:
+        on = _stream_on(stream, device)
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(on)
+
+
 # ---------------------------------------------------------------- config
 
 OVERFLOW = {"drop": 0, "reroute": 1}
@@ -468,6 +485,10 @@ def moe_trace_end(cap: int = 64) -> List[Tuple[str, int, float]]:
 
 
 # ---------------------------------------------------------------- buffers (device memory plumbing)
+#
+# The calls below that allocate their results take a stream.  A given one is ordered after
+# the current one where something is allocated, and what a call uses is kept until the
+# stream is done with it; the order of inputs, and of what reads the results, is the caller's.
 
 def stats_dict(stats: torch.Tensor) -> Dict[str, float]:
     v = stats.cpu().tolist()
@@ -498,7 +519,9 @@ def pack_weights(cfg: MoEConfig, w1, w3, w2, shared: bool = False, stream=None):
     else:
         W13 = torch.empty((n, 2 * hid, d), dtype=w1.dtype, device=w1.device)
         W2p = torch.empty((n, d, hid), dtype=w1.dtype, device=w1.device)
+    _after_current(stream, w1.device)
     moe_pack_weights(cfg, 1 if shared else 0, w1, w3, w2, W13, W2p, stream)
+    _keep(stream, w1.device, (w1, w3, w2, W13, W2p))
     return W13, W2p
 
 
@@ -507,9 +530,11 @@ def forward(cfg: MoEConfig, x, Wr, bias, W13, W2p, W13s=None, W2s=None, bufs=Non
     """One moe_forward call; returns the buffers dict (allocated if not given)."""
     if bufs is None:
         bufs = alloc_layer(cfg, x.device)
+        _after_current(stream, x.device)
     moe_forward(cfg, x, Wr, bias if cfg.has_bias else None, W13, W2p, W13s, W2s, bufs["out"],
                 bufs["topk_idx"], bufs["topk_gate"], bufs["routed"], bufs["kept"],
                 bufs["slot_of"], bufs["stats"] if with_stats else None, bufs["ws"], stream)
+    _keep(stream, x.device, (x, Wr, bias, W13, W2p, W13s, W2s, *bufs.values()))
     return bufs
 
 
@@ -522,7 +547,9 @@ def pack_weights_backward(cfg: MoEConfig, w1, w3, w2, shared: bool = False, stre
     else:
         W13t = torch.empty((n, d, 2 * hid), dtype=w1.dtype, device=w1.device)
         W2t = torch.empty((n, hid, d), dtype=w1.dtype, device=w1.device)
+    _after_current(stream, w1.device)
     moe_pack_weights(cfg, 3 if shared else 2, w1, w3, w2, W13t, W2t, stream)
+    _keep(stream, w1.device, (w1, w3, w2, W13t, W2t))
     return W13t, W2t
 
 
@@ -552,11 +579,14 @@ def backward(cfg: MoEConfig, grad_out, aux_coef, x, Wr, bias, W13t, W2t, W13st, 
     """One moe_backward call after forward(...) filled `bufs` (cfg.train = 1)."""
     if grads is None:
         grads = alloc_grads(cfg, x.device)
+        _after_current(stream, x.device)
     moe_backward(cfg, grad_out, aux_coef, x, Wr, bias if cfg.has_bias else None, W13t, W2t,
                  W13st, W2st, bufs["topk_idx"], bufs["topk_gate"], bufs["routed"], bufs["kept"],
                  bufs["slot_of"], bufs["ws"], grads["dx"], grads["dWr"], grads["db"],
                  grads["dW13"], grads["dW2p"], grads.get("dW13s"), grads.get("dW2s"),
                  grads["dlogits"], grads["bws"], stream)
+    _keep(stream, x.device, (grad_out, x, Wr, bias, W13t, W2t, W13st, W2st, *bufs.values(),
+                             *grads.values()))
     return grads
 
 
@@ -593,15 +623,13 @@ def _q4_convert(fn, cfg, group, shared, src, dst, fresh, stream):
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             return _q4_convert(fn, cfg, group, shared, src, dst, fresh, stream)
-    current = torch.cuda.current_stream(dev)
-    on = current if stream is None else _stream_on(stream, dev)
-    if fresh and on != current:
-        on.wait_stream(current)
+    if fresh:
+        _after_current(stream, dev)
+    on = torch.cuda.current_stream(dev) if stream is None else stream
+    on = on.cuda_stream if isinstance(on, torch.cuda.Stream) else int(on)
     _check(fn(ctypes.byref(cfg), 1 if shared else 0, group, src[0].data_ptr(), src[1].data_ptr(),
-              dst[0].data_ptr(), dst[1].data_ptr(), on.cuda_stream))
-    if stream is not None:
-        for t in (*src, *dst):
-            t.record_stream(on)
+              dst[0].data_ptr(), dst[1].data_ptr(), on))
+    _keep(stream, dev, (*src, *dst))
     return dst
 
 
