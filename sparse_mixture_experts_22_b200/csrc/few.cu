@@ -10,11 +10,14 @@
 // in the workspace; the combine adds a token's rows in a fixed order, so the
 // result does not depend on which CTA finished first.
 //
-// Measured (a call in a stream of calls, launches included): one token, d = 4096, h =
-// 14336, 2 of 8 experts 118-122 us in bf16 (5.8-6.0 TB/s of weights), 50 us on 4 bits (3.6
-// TB/s); eight tokens over 160 experts and two shared ones, d = 5120, h = 1536, 334-343 us
-// (6.1-6.3 TB/s) and 144 us.  In bf16 HBM bounds it, on 4 bits the instructions of the
-// products; 10 to 12 us are the router, the routing and the combine.
+// Measured (a call in a stream of calls, launches included, by box and batch): one token,
+// d = 4096, h = 14336, 2 of 8 experts 117-122 us in bf16 (5.8-6.0 TB/s of weights), 50 us
+// on 4 bits (3.6 TB/s); eight tokens over 160 experts and two shared ones, d = 5120, h =
+// 1536, 319-343 us (6.1-6.5 TB/s) and 151-167 us; sixteen tokens on the first layer 435 us
+// (6.4 TB/s) and 219-231 us.  In bf16 HBM bounds it.  On 4 bits no unit is full (issue
+// slots 50 to 60 %, HBM 36 to 48 %, 8-bit products 13 to 20 %): what is left is latency
+// between the instructions of four multiplying warps a scheduler.  10 to 12 us are the
+// router, the routing and the combine.
 #include <math.h>
 
 #include <atomic>
@@ -367,7 +370,10 @@ __device__ __forceinline__ float lds_bf16(uint32_t addr) {
 // w2 (16 a warp) by the part's columns against H; the products of one expert go
 // to the part's own rows of the partial outputs.
 //
-// bf16 weights: m16n8k16 products with fp32 sums, H as two bf16 parts.
+// bf16 weights: m16n8k16 products with fp32 sums, H as two bf16 parts: each unit is off by
+// 2^-17 of itself at most, where the store of out rounds to 2^-8.  (A third part: one
+// token wide 122.6 us against 116.7, and 1.0 instead of 1.5 in 1000 elements of out that
+// are not the 64-bit value's rounding; the others are the fp32 sums'.)
 //
 // 4-bit weights: the products are exact.  A row of x is an integer of 31 bits
 // times a power of two (of the row's largest magnitude: the rounding is 2^-30 of
@@ -1251,9 +1257,9 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
 // token: 16 groups of 8 lanes share the rows, so that many of them are in flight at
 // once (a token of a small batch has as many rows as there are parts).  128 threads
 // of 32 registers and little shared memory find room beside the expert kernel's
-// block, so that they are there when it ends (8 tokens over 160 experts, d = 5120: the
-// layer 336.7 us with blocks of 256 threads that do not, 324.5 with these; 16 tokens
-// and 4 bits, d = 4096: 242.7 and 232.7).
+// block, so that they are there when it ends (8 tokens over 160 experts, d = 5120, both
+// in one run: the layer 336.7 us with blocks of 256 threads that do not, 324.5 with
+// these; 16 tokens and 4 bits, d = 4096: 4 % less).
 constexpr int CB_COLS = 32;
 constexpr int CB_GROUPS = 16;
 

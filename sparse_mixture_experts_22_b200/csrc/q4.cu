@@ -8,15 +8,17 @@
 // weight is off by 2^-9 of itself at most.  Read back, q s is exact in fp32 (4
 // bits times 8) and rounded once to bf16.
 //
-// One pass, bound by memory.  A warp takes 16 rows x 128 columns: lane (half,
-// c) reads the eight weights 8c.. of row i (half 0) and row i + 8 (half 1) for i
-// = 0..7, so that a row's 256 bytes are one access and eight are in flight.  The
-// two halves exchange one word of codes for each, which leaves every lane a word
-// in fragment order.  d = 4096, h = 14336, 8 experts,
-// group 128 (3.5 GB): packed to 4 bits in 603 us and back in 537, 5.9 and 6.6 TB/s.
-// What counts is bytes in flight: a tile a warp (a grid of 8 blocks an SM that steps
-// over the tiles took 693 and 623), eight rows' loads before the first is used (four:
-// 691), and four blocks of 64 registers an SM rather than three of 74 (743).
+// One pass.  A warp takes 16 rows x 128 columns: lane (half, c) reads the eight
+// weights 8c.. of row i (half 0) and row i + 8 (half 1) for i = 0..7, so that a row's
+// 256 bytes are one access and eight are in flight.  The two halves exchange one word
+// of codes for each, which leaves every lane a word in fragment order.  d = 4096, h =
+// 14336, 8 experts, group 128 (3.5 GB): packed to 4 bits in 587-654 us by box and back in
+// 537-555, 5.5-6.1 and 6.3-6.6 TB/s.  Reading back is bound by memory, packing by memory
+// and instructions alike (issue slots 73 %, ALU 68 %, HBM 68 %).
+// What counts is bytes in flight (each against 603 and 537 then): a tile a warp (a grid of 8
+// blocks an SM that steps over the tiles took 693 and 623), eight rows' loads before the
+// first is used (four: 691), and four blocks of 64 registers an SM rather than three of
+// 74 (743).
 #include "common.cuh"
 #include "few.h"
 #include "kernels.h"
