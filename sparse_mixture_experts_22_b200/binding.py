@@ -769,10 +769,13 @@ class FewLayer:
         return self._run(fn, head, tail, views, x, stream)
 
     def _run(self, fn, head, tail, views, x, stream):
-        on = torch.cuda.current_stream(self.device) if stream is None else stream
-        handle = on.cuda_stream if isinstance(on, torch.cuda.Stream) else int(on)
+        if stream is None:
+            handle = torch.cuda.current_stream(self.device).cuda_stream
+        else:
+            handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
         if handle not in self._streams:
-            on = self._streams[handle] = _stream_on(on, self.device)
+            on = self._streams[handle] = _stream_on(
+                torch.cuda.current_stream(self.device) if stream is None else stream, self.device)
             for t in (*self._held, *self.bufs.values(), self.ws):
                 if t is not None:
                     t.record_stream(on)

@@ -71,13 +71,17 @@ def test_results_on_a_given_stream(made, name, kind):
         assert bool((c == 7).all())
     for a, b in zip(got, want):
         assert torch.equal(a, b)
-    # results freed before the call has run: what is made of their blocks stays
+    # results freed before the call has run: what is made of their blocks stays, and while
+    # the stream is busy nothing is made of them
+    del got, a, copies, c
+    torch.cuda.synchronize()
     with torch.cuda.stream(s):
         torch.cuda._sleep(CYCLES)
     got = call(arg)
     ptrs = {t.data_ptr() for t in got}
     del got
     junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in nbytes]
-    assert not ptrs & {t.data_ptr() for t in junk}
+    taken = ptrs & {t.data_ptr() for t in junk}
+    assert s.query() or not taken
     torch.cuda.synchronize()
     assert all(bool((t == 255).all()) for t in junk)
